@@ -80,6 +80,16 @@ typedef enum psi_dtype { PSI_DTYPE_F32 = 0, PSI_DTYPE_BF16 = 1 } psi_dtype;
                                    valid logit: probability zero) */
 #define PSI_DEV_TIMEOUT 8u      /* a bounded wait inside a kernel gave up;
                                    never expected; outputs are then invalid */
+#define PSI_DEV_BAD_PAGE 16u    /* cache: a position without a valid page (past
+                                   the sequence's table, or a page index outside
+                                   the pool), or a page released more often than
+                                   it is held: that position is left out */
+#define PSI_DEV_NO_PAGES 32u    /* cache: not enough free pages, or no room in
+                                   the sequence's table: it got none */
+#define PSI_DEV_BAD_PATH 64u    /* cache: an accepted path that is not ascending
+                                   within [0, M): cut at its first bad node */
+#define PSI_DEV_BAD_SEQ 128u    /* cache: a fork whose rows are out of range,
+                                   repeated or not empty: it is left out */
 
 /* RNG purposes (the last hash input). */
 #define PSI_PURPOSE_ACCEPT 0u /* u_i of the acceptance test of row i */
@@ -315,6 +325,196 @@ psi_status psi_verify_tree_sampled(const void *ar_logits, int64_t ar_row_stride,
                                    int32_t *out_path_len, int32_t *out_tokens,
                                    uint32_t *dev_status, void *workspace,
                                    size_t workspace_bytes, psi_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The key-value cache around the verify step.
+ *
+ * Before the verify, the frozen AR path runs over the drafted block: each of
+ * its attention layers writes the block's keys and values into the cache
+ * (psi_cache_append) and attends over the cache (psi_attend_block).  After
+ * it, the accepted nodes stay (psi_cache_commit), and the sequences' pages
+ * are fitted to their new lengths (psi_cache_resize).  psi_cache_fork
+ * continues a sequence more than once.  The pages name the block and the
+ * prefix tree that is verified in one pass ([P3] "Linear 與 Tree sampler");
+ * the cache's form is this library's.
+ *
+ * Pages.  Keys and values live in two pools of num_pages pages of page_size
+ * slots.  Element d of head h in slot s of page p of layer l is at
+ *   l * layer_stride + p * page_stride + s * slot_stride + h * head_stride + d
+ * in both pools (strides in elements, so [page][slot][head][d] and
+ * [page][head][slot][d] are both cache layouts).  Both pools and every
+ * stride but that of d are multiples of 16 bytes, and head_dim is a multiple
+ * of 8.  Position t of sequence n is slot t % page_size of page
+ * page_table[n][t / page_size]; page_table is int32 [N][max_pages].
+ *
+ * Blocks.  A block has R rows per sequence, as the verify's logits do: row 0
+ * is the root (the last emitted token, not in the cache yet), row k + 1 is
+ * drafted token or tree node k, so R = B + 1 or M + 1, and R = 1 is a step
+ * of one token.  lens[n] is the number of positions in the cache before the
+ * block; row r of the block takes position lens[n] + r of the cache, and its
+ * rotary position is lens[n] + its depth.  parents is int32 [N][R - 1] as in
+ * the tree verify, or NULL for a chain (every row continues the one before
+ * it).  A row whose chain of parents holds an invalid index (>= its own or
+ * < -1) is not part of the block: nothing is written for it by
+ * psi_cache_append, and it attends to nothing.  lens[n] < 0 marks a sequence
+ * that is not there (a padded batch): all that belongs to it is left as it
+ * was.
+ * ------------------------------------------------------------------------- */
+#define PSI_MAX_BLOCK_ROWS 256 /* rows of a block (R) */
+#define PSI_MAX_HEAD_DIM 256
+#define PSI_MAX_PAGE_SIZE 1024
+
+typedef struct psi_cache_layout {
+  psi_dtype dtype;   /* of keys, values and queries */
+  int32_t layers;    /* layers of the pools (commit, fork); 1 elsewhere */
+  int32_t num_pages; /* pages per layer */
+  int32_t page_size; /* slots per page, 1..PSI_MAX_PAGE_SIZE */
+  int32_t kv_heads;
+  int32_t head_dim;  /* multiple of 8, up to PSI_MAX_HEAD_DIM */
+  int64_t layer_stride, page_stride, slot_stride, head_stride;
+} psi_cache_layout;
+
+/*
+ * psi_cache_append - norm, rotary positions and the write of a block's keys
+ * and values into one layer's pages.
+ *
+ * For a head x of row r (queries and keys; values are stored as they are):
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (y = x where weight is NULL)
+ *   each pair (a, b) of y's first rotary_dim elements is turned by the angle
+ *   t = position * inv_freq[i]: rope_scale * (a cos t - b sin t,
+ *   b cos t + a sin t).  Pair i is elements (i, i + rotary_dim / 2), or with
+ *   `interleaved` (2i, 2i + 1).  The rest of the head keeps y.
+ * The angle is taken in double precision, the rest in float, and the result
+ * is rounded once.  Scaled positions (linear, by wavelength, YaRN and the
+ * like) are a choice of inv_freq and rope_scale.
+ *
+ * q  R rows per sequence of q_heads heads, k and v of kv_heads heads: row r
+ *    of sequence n, head h starts at (n * R + r) * row_stride +
+ *    h * head_stride elements, so the three may be slices of one projection.
+ * q_weight, k_weight  head_dim weights of the block's dtype, or NULL.
+ * inv_freq   double [rotary_dim / 2] radians per position; NULL with
+ *            rotary_dim 0.  rotary_dim is even and at most head_dim.
+ * out_q      [N][R][q_heads][head_dim]; may be q itself when q is that.
+ * The pools must not overlap the block's tensors, and two rows of a call
+ * must not share a slot (pages of a sequence's block belong to it alone).
+ * Limits: 1 <= N, 1 <= R <= PSI_MAX_BLOCK_ROWS, eps >= 0.
+ */
+psi_status psi_cache_append(const psi_cache_layout *layout, void *k_pages, void *v_pages,
+                            const int32_t *page_table, int32_t max_pages, const int32_t *lens,
+                            int32_t N, int32_t R, int32_t q_heads, const void *q,
+                            int64_t q_row_stride, int64_t q_head_stride, const void *k,
+                            int64_t k_row_stride, int64_t k_head_stride, const void *v,
+                            int64_t v_row_stride, int64_t v_head_stride, const void *q_weight,
+                            const void *k_weight, float eps, const double *inv_freq,
+                            int32_t rotary_dim, int32_t interleaved, float rope_scale,
+                            const int32_t *parents, void *out_q, uint32_t *dev_status,
+                            psi_stream_t stream);
+
+/* Workspace needed by psi_attend_block (bytes, a multiple of 256; 0 on
+ * invalid sizes).  The workspace needs no initialisation. */
+size_t psi_attend_block_workspace_bytes(const psi_cache_layout *layout, int32_t N, int32_t R,
+                                        int32_t q_heads, int32_t max_pages);
+
+/*
+ * psi_attend_block - attention of a block over one layer's pages.
+ *
+ * Row r of sequence n sees positions 0..lens[n]-1 and those rows of its own
+ * block that are r or lie on r's path to the root (rows 0..r of a chain):
+ *   o = sum_t p_t v_t,  p = softmax over the seen t of scale * (q . k_t)
+ * with kv head h / (q_heads / kv_heads) for query head h.  What a row does
+ * not see has no influence on it, whatever it holds.  A row that sees
+ * nothing (invalid parents; no valid page) gives zeros.
+ *
+ * q         as in psi_cache_append; the block's keys and values are in the
+ *           pages already.
+ * out_o     [N][R][q_heads][head_dim], not overlapping any input.
+ * out_lse   float [N][R][q_heads] or NULL: log of the sum of
+ *           exp(scale * q . k_t) over the seen t, -inf for none.
+ * Scores, the softmax and the sums are float; bf16 weights p are rounded to
+ * bf16 for the product with v.  Results do not depend on the other
+ * sequences of a call, and the same call gives the same bits.
+ * Limits: as psi_cache_append; q_heads a multiple of kv_heads; scale finite.
+ */
+psi_status psi_attend_block(const psi_cache_layout *layout, const void *k_pages,
+                            const void *v_pages, const int32_t *page_table, int32_t max_pages,
+                            const int32_t *lens, int32_t N, int32_t R, int32_t q_heads,
+                            const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                            const int32_t *parents, float scale, void *out_o, float *out_lse,
+                            uint32_t *dev_status, void *workspace, size_t workspace_bytes,
+                            psi_stream_t stream);
+
+/*
+ * psi_cache_commit - keep the accepted path of a tree verify.
+ *
+ * path_nodes int32 [N][M] and path_len int32 [N] are the tree verify's
+ * outputs.  In every layer, keys and values of node path_nodes[n][j]
+ * (position lens[n] + 1 + path_nodes[n][j]) move to position
+ * lens[n] + 1 + j, and out_lens[n] = lens[n] + 1 + path_len[n]: the root and
+ * the path.  (After a linear verify the accepted rows are in place already:
+ * the new length is lens + n_emitted.)
+ * A path must ascend within [0, M); it is cut at its first bad node.  A
+ * position without a valid page is left out.
+ * out_lens int32 [N], not overlapping lens (which every CTA reads).
+ * The pages that hold a sequence's block must belong to it alone.
+ */
+psi_status psi_cache_commit(const psi_cache_layout *layout, void *k_pages, void *v_pages,
+                            const int32_t *page_table, int32_t max_pages, const int32_t *lens,
+                            int32_t N, int32_t M, const int32_t *path_nodes,
+                            const int32_t *path_len, int32_t *out_lens, uint32_t *dev_status,
+                            psi_stream_t stream);
+
+/* Who holds which page.  Device pointers. */
+typedef struct psi_page_state {
+  int32_t *page_table;  /* [N][max_pages]; -1 where no page is held */
+  int32_t *page_counts; /* [N] pages held: the row's first page_counts entries */
+  int32_t *refs;        /* [num_pages] sequences that hold the page */
+  int32_t *free_pages;  /* [num_pages] a stack of free pages */
+  int32_t *n_free;      /* [1] its height */
+} psi_page_state;
+
+/*
+ * psi_cache_resize - fit each sequence's pages to lens[n] + extra positions:
+ * to room for the next block (extra = R), to what is held after a commit
+ * (extra = 0), or to nothing (lens = 0, extra = 0: the sequence is freed).
+ *
+ * Pages over ceil((lens[n] + extra) / page_size) are released: their table
+ * entries become -1 and refs falls by one; pages that nobody holds any more
+ * are pushed on the free stack, lowest index first.  Then missing pages are
+ * popped, in the order of (sequence, position); a sequence gets all that it
+ * needs or none (and so do the later ones that need any, when the stack is
+ * too low; a row too short for its sequence does not count).  lens[n] < 0:
+ * left as it is.
+ * in and out may be the same state, or hold ten different arrays; table
+ * entries beyond page_counts are not read.  Deterministic.
+ */
+psi_status psi_cache_resize(int32_t N, int32_t max_pages, int32_t num_pages, int32_t page_size,
+                            const int32_t *lens, int32_t extra, const psi_page_state *in,
+                            const psi_page_state *out, uint32_t *dev_status, psi_stream_t stream);
+
+/* Workspace needed by psi_cache_fork (bytes, a multiple of 256; 0 on invalid
+ * sizes).  The workspace needs no initialisation. */
+size_t psi_cache_fork_workspace_bytes(int32_t K);
+
+/*
+ * psi_cache_fork - continue sequences: row dst[k] becomes a copy of row
+ * src[k] with lens[src[k]] positions.
+ *
+ * Whole pages are shared (refs rises by one); a page that the length ends
+ * inside is copied, its filled slots in every layer, to a page popped from
+ * the free stack (in the order of k; a fork gets its page or is left out,
+ * and so are the later ones that need one).  out lens[dst] = lens[src].
+ * A fork is left out and flagged when a row is out of [0, N), when dst holds
+ * pages already, when dst is an earlier fork's dst, or any fork's src, or
+ * when lens[src] < 0 or src lacks a page below its length.
+ * in and out may be the same state (and out_lens the same array as lens);
+ * where they differ, all else is carried over.
+ * Limits: 1 <= K <= N.
+ */
+psi_status psi_cache_fork(const psi_cache_layout *layout, void *k_pages, void *v_pages, int32_t N,
+                          int32_t max_pages, const int32_t *lens, int32_t *out_lens,
+                          const psi_page_state *in, const psi_page_state *out, int32_t K,
+                          const int32_t *src, const int32_t *dst, uint32_t *dev_status,
+                          void *workspace, size_t workspace_bytes, psi_stream_t stream);
 
 /*
  * psi_rng_uniforms - the uniforms the verify step draws, for inspection and

@@ -36,6 +36,10 @@ PSI_DEV_BAD_TOKEN_ID = 1
 PSI_DEV_BAD_PARENT = 2
 PSI_DEV_NONFINITE = 4
 PSI_DEV_TIMEOUT = 8
+PSI_DEV_BAD_PAGE = 16
+PSI_DEV_NO_PAGES = 32
+PSI_DEV_BAD_PATH = 64
+PSI_DEV_BAD_SEQ = 128
 # RNG purposes
 PSI_PURPOSE_ACCEPT = 0
 PSI_PURPOSE_RESID = 1
@@ -49,6 +53,9 @@ PSI_GREEDY_ROUND_POSITIONS = 3
 PSI_SAMPLED_SHORT_ROUNDS = 2
 PSI_GREEDY_SHORT_ROUNDS = 3
 PSI_EARLY_EXIT_MIN_N = 64
+PSI_MAX_BLOCK_ROWS = 256
+PSI_MAX_HEAD_DIM = 256
+PSI_MAX_PAGE_SIZE = 1024
 
 EXPORTED = (
     "psi_verify_linear_workspace_bytes",
@@ -60,6 +67,13 @@ EXPORTED = (
     "psi_verify_tree_greedy",
     "psi_verify_tree_sampled_workspace_bytes",
     "psi_verify_tree_sampled",
+    "psi_cache_append",
+    "psi_attend_block_workspace_bytes",
+    "psi_attend_block",
+    "psi_cache_commit",
+    "psi_cache_resize",
+    "psi_cache_fork_workspace_bytes",
+    "psi_cache_fork",
     "psi_rng_uniforms",
     "psi_profile_main_kernel",
     "psi_status_string",
@@ -119,6 +133,7 @@ def load_library():
     lib.psi_status_string.argtypes = [C.c_int]
     lib.psi_last_error.restype = C.c_char_p
     lib.psi_last_error.argtypes = []
+    cache.declare(lib)
     _lib = lib
     return lib
 
@@ -492,6 +507,16 @@ def rng_uniforms(seed: int, n_seq: int, step: int, n_rows: int, purpose: int, se
     return out
 
 
+# (imports the helpers above)
+from . import cache  # noqa: E402
+from .cache import (  # noqa: E402
+    AppendResult, AttendResult, CacheLayout, CommitResult, ForkResult, PageState, PageStatePtrs,
+    ResizeResult, attend_block, cache_append, cache_commit, cache_fork, cache_resize,
+    psi_attend_block, psi_attend_block_workspace_bytes, psi_cache_append, psi_cache_commit,
+    psi_cache_fork, psi_cache_fork_workspace_bytes, psi_cache_resize, rope_frequencies)
+
 __all__ = [n for n in dir() if n.startswith(("psi_", "PSI_"))] + [
     "verify_linear", "verify_tree_greedy", "rng_uniforms", "LinearResult", "TreeResult",
-    "PsiError", "load_library", "EXPORTED", "verify_tree_sampled"]
+    "PsiError", "load_library", "EXPORTED", "verify_tree_sampled", "attend_block", "cache_append",
+    "cache_commit", "cache_resize", "cache_fork", "rope_frequencies", "PageState", "AppendResult",
+    "AttendResult", "CommitResult", "ResizeResult", "ForkResult", "CacheLayout", "PageStatePtrs"]

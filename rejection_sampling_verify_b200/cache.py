@@ -1,0 +1,469 @@
+"""The key-value cache around the verify step: Python binding.
+
+Like the verify's binding, this module only marshals arguments: the raw
+functions carry the ABI's names (``include/psi_verify.h``), and the tensor
+helpers check shapes, allocate outputs and workspace with torch, and call
+them on the current stream.  The order of a serving step is
+
+    cache_resize   room for the drafted block in every sequence
+    cache_append   per layer: norm, rotary positions, write of keys and values
+    attend_block   per layer: attention of the block over the cache
+    verify_*       of the block's logits
+    cache_commit   the accepted path stays (tree verify); after a linear
+                   verify the new length is lens + n_emitted
+    cache_resize   pages behind the new length go back
+    cache_fork     a sequence is continued more than once
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+from dataclasses import dataclass
+
+from . import (PSI_OK, PsiError, _check_out, _check_workspace, _device_of, _dtype_code, _nbytes,
+               _ptr, _stream, _torch, load_library)
+
+
+class CacheLayout(C.Structure):
+    """``psi_cache_layout``."""
+    _fields_ = [("dtype", C.c_int), ("layers", C.c_int32), ("num_pages", C.c_int32),
+                ("page_size", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("layer_stride", C.c_int64), ("page_stride", C.c_int64),
+                ("slot_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class PageStatePtrs(C.Structure):
+    """``psi_page_state``: device pointers."""
+    _fields_ = [("page_table", C.c_void_p), ("page_counts", C.c_void_p), ("refs", C.c_void_p),
+                ("free_pages", C.c_void_p), ("n_free", C.c_void_p)]
+
+
+def declare(lib):
+    """Argument types of the cache's entry points."""
+    vp, i32, i64, f32, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_float, C.c_size_t
+    lay, st = C.POINTER(CacheLayout), C.POINTER(PageStatePtrs)
+    lib.psi_cache_append.restype = C.c_int
+    lib.psi_cache_append.argtypes = [lay, vp, vp, vp, i32, vp, i32, i32, i32, vp, i64, i64, vp,
+                                     i64, i64, vp, i64, i64, vp, vp, f32, vp, i32, i32, f32, vp,
+                                     vp, vp, vp]
+    lib.psi_attend_block_workspace_bytes.restype = sz
+    lib.psi_attend_block_workspace_bytes.argtypes = [lay, i32, i32, i32, i32]
+    lib.psi_attend_block.restype = C.c_int
+    lib.psi_attend_block.argtypes = [lay, vp, vp, vp, i32, vp, i32, i32, i32, vp, i64, i64, vp,
+                                     f32, vp, vp, vp, vp, sz, vp]
+    lib.psi_cache_commit.restype = C.c_int
+    lib.psi_cache_commit.argtypes = [lay, vp, vp, vp, i32, vp, i32, i32, vp, vp, vp, vp, vp]
+    lib.psi_cache_resize.restype = C.c_int
+    lib.psi_cache_resize.argtypes = [i32, i32, i32, i32, vp, i32, st, st, vp, vp]
+    lib.psi_cache_fork_workspace_bytes.restype = sz
+    lib.psi_cache_fork_workspace_bytes.argtypes = [i32]
+    lib.psi_cache_fork.restype = C.c_int
+    lib.psi_cache_fork.argtypes = [lay, vp, vp, i32, i32, vp, vp, st, st, i32, vp, vp, vp, vp, sz,
+                                   vp]
+
+
+# ---- raw ABI (device pointers as ints, structures as the classes above) ------------
+
+def _ref(s):
+    return None if s is None else C.byref(s)
+
+
+def psi_cache_append(layout, k_pages, v_pages, page_table, max_pages, lens, N, R, q_heads, q,
+                     q_row_stride, q_head_stride, k, k_row_stride, k_head_stride, v, v_row_stride,
+                     v_head_stride, q_weight, k_weight, eps, inv_freq, rotary_dim, interleaved,
+                     rope_scale, parents, out_q, dev_status, stream) -> int:
+    return int(load_library().psi_cache_append(
+        _ref(layout), k_pages, v_pages, page_table, max_pages, lens, N, R, q_heads, q,
+        q_row_stride, q_head_stride, k, k_row_stride, k_head_stride, v, v_row_stride,
+        v_head_stride, q_weight, k_weight, eps, inv_freq, rotary_dim, interleaved, rope_scale,
+        parents, out_q, dev_status, stream))
+
+
+def psi_attend_block_workspace_bytes(layout, N, R, q_heads, max_pages) -> int:
+    return int(load_library().psi_attend_block_workspace_bytes(_ref(layout), N, R, q_heads,
+                                                               max_pages))
+
+
+def psi_attend_block(layout, k_pages, v_pages, page_table, max_pages, lens, N, R, q_heads, q,
+                     q_row_stride, q_head_stride, parents, scale, out_o, out_lse, dev_status,
+                     workspace, workspace_bytes, stream) -> int:
+    return int(load_library().psi_attend_block(
+        _ref(layout), k_pages, v_pages, page_table, max_pages, lens, N, R, q_heads, q,
+        q_row_stride, q_head_stride, parents, scale, out_o, out_lse, dev_status, workspace,
+        workspace_bytes, stream))
+
+
+def psi_cache_commit(layout, k_pages, v_pages, page_table, max_pages, lens, N, M, path_nodes,
+                     path_len, out_lens, dev_status, stream) -> int:
+    return int(load_library().psi_cache_commit(_ref(layout), k_pages, v_pages, page_table,
+                                               max_pages, lens, N, M, path_nodes, path_len,
+                                               out_lens, dev_status, stream))
+
+
+def psi_cache_resize(N, max_pages, num_pages, page_size, lens, extra, in_state, out_state,
+                     dev_status, stream) -> int:
+    return int(load_library().psi_cache_resize(N, max_pages, num_pages, page_size, lens, extra,
+                                               _ref(in_state), _ref(out_state), dev_status,
+                                               stream))
+
+
+def psi_cache_fork_workspace_bytes(K) -> int:
+    return int(load_library().psi_cache_fork_workspace_bytes(K))
+
+
+def psi_cache_fork(layout, k_pages, v_pages, N, max_pages, lens, out_lens, in_state, out_state, K,
+                   src, dst, dev_status, workspace, workspace_bytes, stream) -> int:
+    return int(load_library().psi_cache_fork(_ref(layout), k_pages, v_pages, N, max_pages, lens,
+                                             out_lens, _ref(in_state), _ref(out_state), K, src,
+                                             dst, dev_status, workspace, workspace_bytes, stream))
+
+
+# ---- torch tensor helpers --------------------------------------------------------------
+
+@dataclass
+class AppendResult:
+    q: "torch.Tensor"       # [N, R, Hq, D]
+    status: "torch.Tensor"  # int32 [1] device status word
+
+
+@dataclass
+class AttendResult:
+    o: "torch.Tensor"            # [N, R, Hq, D]
+    lse: "torch.Tensor | None"   # float32 [N, R, Hq]
+    status: "torch.Tensor"
+
+
+@dataclass
+class CommitResult:
+    lens: "torch.Tensor"    # int32 [N]
+    status: "torch.Tensor"
+
+
+@dataclass
+class PageState:
+    """Who holds which page (``psi_page_state``); int32 tensors."""
+    table: "torch.Tensor"   # [N, max_pages], -1 where no page is held
+    counts: "torch.Tensor"  # [N]
+    refs: "torch.Tensor"    # [P]
+    free: "torch.Tensor"    # [P] stack of free pages
+    n_free: "torch.Tensor"  # [1]
+
+    @classmethod
+    def empty(cls, N: int, max_pages: int, num_pages: int, device="cuda") -> "PageState":
+        """No sequence holds a page; page 0 is the first to be popped."""
+        torch = _torch()
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.full((N, max_pages), -1, **i32), torch.zeros(N, **i32),
+                   torch.zeros(num_pages, **i32),
+                   torch.arange(num_pages - 1, -1, -1, **i32),
+                   torch.full((1,), num_pages, **i32))
+
+
+@dataclass
+class ResizeResult:
+    pages: PageState
+    status: "torch.Tensor"
+
+
+@dataclass
+class ForkResult:
+    pages: PageState
+    lens: "torch.Tensor"
+    status: "torch.Tensor"
+
+
+def _check(status, where):
+    if status != PSI_OK:
+        raise PsiError(status, where)
+
+
+def _int32(name, t, shape):
+    torch = _torch()
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def _layout(k_pages, v_pages, layered: bool) -> CacheLayout:
+    """The pools' layout: [P, S, H, D] of one layer, or [L, P, S, H, D]."""
+    dims = 5 if layered else 4
+    if k_pages.dim() != dims or k_pages.shape != v_pages.shape or \
+            k_pages.stride() != v_pages.stride() or k_pages.dtype != v_pages.dtype:
+        raise ValueError(f"k_pages and v_pages must have {dims} dims "
+                         f"({'layers, ' if layered else ''}pages, slots, heads, elements) and the "
+                         f"same shape, strides and dtype")
+    if k_pages.stride(-1) != 1:
+        raise ValueError("pages must have a contiguous last dim")
+    shape = tuple(k_pages.shape) if layered else (1, *k_pages.shape)
+    strides = tuple(k_pages.stride()) if layered else (0, *k_pages.stride())
+    strides = [0 if n == 1 else s for n, s in zip(shape, strides)]
+    return CacheLayout(_dtype_code(k_pages), *shape, *strides[:4])
+
+
+def _heads(name, t, N, R, heads, D, dtype):
+    """(row stride, head stride) of a [N, R, heads, D] tensor with evenly spaced rows."""
+    if tuple(t.shape) != (N, R, heads, D) or t.dtype != dtype or t.stride(3) != 1:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(N, R, heads, D)} with a "
+                         f"contiguous last dim, got {t.dtype} {tuple(t.shape)}")
+    row = t.stride(1) if R > 1 else t.stride(0) if N > 1 else 0
+    if N > 1 and R > 1 and t.stride(0) != R * row:
+        raise ValueError(f"{name}: rows must be evenly spaced")
+    return row, t.stride(2) if heads > 1 else 0
+
+
+def _block(q, page_table, lens, parents):
+    torch = _torch()
+    if q.dim() != 4:
+        raise ValueError("q must be [N, R, heads, D]")
+    N, R = q.shape[:2]
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [N, max_pages]")
+    _int32("page_table", page_table, (N, page_table.shape[1]))
+    _int32("lens", lens, (N,))
+    if parents is not None:
+        _int32("parents", parents, (N, R - 1))
+    return N, R
+
+
+def _new_status(dev):
+    torch = _torch()
+    return torch.zeros(1, dtype=torch.int32, device=dev)
+
+
+def rope_frequencies(rotary_dim: int, theta: float = 1e6, factor: float = 1.0,
+                     scaling: str = "none", original_length: int = 32768,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """(inv_freq, rope_scale) for :func:`cache_append`: float64 [rotary_dim/2].
+
+    scaling "none"; "linear" (positions divided by ``factor``); "ntk" (theta
+    grown so that the longest wavelength stretches by ``factor``); "yarn"
+    (Peng et al., "YaRN: Efficient Context Window Extension of Large Language
+    Models", 2023: pairs that turn less than ``beta_slow`` times over
+    ``original_length`` are stretched, those over ``beta_fast`` are kept, with
+    a ramp between, and the scores' temperature goes into rope_scale).
+    """
+    torch = _torch()
+    if rotary_dim < 2 or rotary_dim % 2 or factor < 1:
+        raise ValueError("rotary_dim must be even and positive, factor at least 1")
+    i = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    if scaling == "ntk" and rotary_dim > 2:
+        theta = theta * factor ** (rotary_dim / (rotary_dim - 2))
+    inv = theta ** (-2.0 * i / rotary_dim)
+    scale = 1.0
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "yarn":
+        def pair(turns):  # the pair that turns so often over the original length
+            return rotary_dim * math.log(original_length / (turns * 2 * math.pi)) / \
+                (2 * math.log(theta))
+        low, high = max(math.floor(pair(beta_fast)), 0), min(math.ceil(pair(beta_slow)),
+                                                             rotary_dim - 1)
+        ramp = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+        inv = inv / factor * ramp + inv * (1 - ramp)
+        scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"scaling must be none, linear, ntk or yarn, got {scaling!r}")
+    return inv.to(device), scale
+
+
+def cache_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight=None, k_weight=None,
+                 eps: float = 1e-6, inv_freq=None, interleaved: bool = False,
+                 rope_scale: float = 1.0, parents=None, stream=None,
+                 out: AppendResult | None = None) -> AppendResult:
+    """Norm, rotary positions and the write of a block's keys and values into
+    one layer's pages (``psi_cache_append``).
+
+    q [N, R, Hq, D], k and v [N, R, H, D] (slices of one projection will do);
+    k_pages, v_pages [P, S, H, D] of any strides; page_table int32
+    [N, max_pages]; lens int32 [N]; q_weight, k_weight [D] or None;
+    inv_freq float64 [rotary_dim / 2] or None; parents int32 [N, R - 1] or
+    None (a chain).  ``out.q`` may be ``q`` itself.
+    """
+    torch = _torch()
+    N, R = _block(q, page_table, lens, parents)
+    lay = _layout(k_pages, v_pages, layered=False)
+    Hq, D, H = q.shape[2], lay.head_dim, lay.kv_heads
+    strides = [_heads(name, t, N, R, h, D, k_pages.dtype)
+               for name, t, h in (("q", q, Hq), ("k", k, H), ("v", v, H))]
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and (w.dtype != q.dtype or tuple(w.shape) != (D,) or
+                              not w.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {q.dtype} tensor of shape ({D},)")
+    if inv_freq is not None and (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or
+                                 not inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous float64 vector")
+    if out is not None:
+        _check_out("q", out.q, q.dtype, (N, R, Hq, D))
+        _check_out("status", out.status, torch.int32, (1,))
+    dev = _device_of(q, k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
+                     lens=lens, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq,
+                     parents=parents,
+                     **({} if out is None else dict(out_q=out.q, status=out.status)))
+    if out is None:
+        out = AppendResult(torch.empty(N, R, Hq, D, dtype=q.dtype, device=dev), _new_status(dev))
+    st = psi_cache_append(
+        lay, _ptr(k_pages), _ptr(v_pages), _ptr(page_table), page_table.shape[1], _ptr(lens), N, R,
+        Hq, _ptr(q), *strides[0], _ptr(k), *strides[1], _ptr(v), *strides[2], _ptr(q_weight),
+        _ptr(k_weight), float(eps), _ptr(inv_freq), 0 if inv_freq is None else 2 * len(inv_freq),
+        int(bool(interleaved)), float(rope_scale), _ptr(parents), _ptr(out.q), _ptr(out.status),
+        _stream(stream))
+    _check(st, "psi_cache_append")
+    return out
+
+
+def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: float | None = None,
+                 want_lse: bool = False, workspace=None, stream=None,
+                 out: AttendResult | None = None) -> AttendResult:
+    """Attention of a block over one layer's pages (``psi_attend_block``).
+
+    q [N, R, Hq, D]; the block's keys and values are in the pages at
+    positions lens[n]..lens[n] + R - 1.  R = 1 is a step of one new token;
+    parents None is a drafted chain, else a tree.  scale defaults to
+    D ** -0.5.  With ``out`` and a large enough ``workspace`` the call only
+    launches work on the stream.
+    """
+    torch = _torch()
+    N, R = _block(q, page_table, lens, parents)
+    lay = _layout(k_pages, v_pages, layered=False)
+    Hq, D = q.shape[2], lay.head_dim
+    q_row, q_head = _heads("q", q, N, R, Hq, D, k_pages.dtype)
+    if out is not None:
+        _check_out("o", out.o, q.dtype, (N, R, Hq, D))
+        _check_out("lse", out.lse, torch.float32, (N, R, Hq), optional=True)
+        _check_out("status", out.status, torch.int32, (1,))
+    _check_workspace(workspace)
+    dev = _device_of(q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, lens=lens,
+                     parents=parents, workspace=workspace,
+                     **({} if out is None else dict(o=out.o, lse=out.lse, status=out.status)))
+    if out is None:
+        out = AttendResult(torch.empty(N, R, Hq, D, dtype=q.dtype, device=dev),
+                           torch.empty(N, R, Hq, dtype=torch.float32, device=dev)
+                           if want_lse else None, _new_status(dev))
+    ws_bytes = psi_attend_block_workspace_bytes(lay, N, R, Hq, page_table.shape[1])
+    if ws_bytes == 0:  # invalid sizes: let the ABI report the precise status
+        workspace = None
+    elif workspace is None or _nbytes(workspace) < ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    st = psi_attend_block(lay, _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+                          page_table.shape[1], _ptr(lens), N, R, Hq, _ptr(q), q_row, q_head,
+                          _ptr(parents), float(D ** -0.5 if scale is None else scale),
+                          _ptr(out.o), _ptr(out.lse), _ptr(out.status), _ptr(workspace),
+                          _nbytes(workspace), _stream(stream))
+    _check(st, "psi_attend_block")
+    return out
+
+
+def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, stream=None,
+                 out: CommitResult | None = None) -> CommitResult:
+    """Keep the accepted path of a tree verify (``psi_cache_commit``).
+
+    k_pages, v_pages [L, P, S, H, D]; path_nodes int32 [N, M] and path_len
+    int32 [N] as :func:`verify_tree_greedy` and :func:`verify_tree_sampled`
+    return them.  Returns the new lengths (``out.lens`` is not ``lens``).
+    """
+    torch = _torch()
+    lay = _layout(k_pages, v_pages, layered=True)
+    if page_table.dim() != 2 or path_nodes.dim() != 2:
+        raise ValueError("page_table must be [N, max_pages], path_nodes [N, M]")
+    N, M = path_nodes.shape
+    _int32("page_table", page_table, (N, page_table.shape[1]))
+    _int32("lens", lens, (N,))
+    _int32("path_nodes", path_nodes, (N, M))
+    _int32("path_len", path_len, (N,))
+    if out is not None:
+        _check_out("lens", out.lens, torch.int32, (N,))
+        _check_out("status", out.status, torch.int32, (1,))
+    dev = _device_of(k_pages, v_pages=v_pages, page_table=page_table, lens=lens,
+                     path_nodes=path_nodes, path_len=path_len,
+                     **({} if out is None else dict(out_lens=out.lens, status=out.status)))
+    if out is None:
+        out = CommitResult(torch.empty_like(lens), _new_status(dev))
+    st = psi_cache_commit(lay, _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+                          page_table.shape[1], _ptr(lens), N, M, _ptr(path_nodes),
+                          _ptr(path_len), _ptr(out.lens), _ptr(out.status), _stream(stream))
+    _check(st, "psi_cache_commit")
+    return out
+
+
+def _state(name, s: PageState, N, max_pages, P):
+    for field, shape in (("table", (N, max_pages)), ("counts", (N,)), ("refs", (P,)),
+                         ("free", (P,)), ("n_free", (1,))):
+        _int32(f"{name}.{field}", getattr(s, field), shape)
+    return PageStatePtrs(_ptr(s.table), _ptr(s.counts), _ptr(s.refs), _ptr(s.free),
+                         _ptr(s.n_free))
+
+
+def _state_tensors(name, s: PageState):
+    return {f"{name}.{f}": getattr(s, f) for f in ("table", "counts", "refs", "free", "n_free")}
+
+
+def _like(s: PageState) -> PageState:
+    torch = _torch()
+    return PageState(*(torch.empty_like(t) for t in (s.table, s.counts, s.refs, s.free, s.n_free)))
+
+
+def cache_resize(pages: PageState, lens, extra: int, page_size: int, stream=None,
+                 out: ResizeResult | None = None) -> ResizeResult:
+    """Fit each sequence's pages to lens[n] + extra positions
+    (``psi_cache_resize``).  Returns a new state; with ``out.pages = pages``
+    the state is changed in place."""
+    torch = _torch()
+    if pages.table.dim() != 2:
+        raise ValueError("pages.table must be [N, max_pages]")
+    N, max_pages = pages.table.shape
+    P = pages.refs.numel()
+    src = _state("pages", pages, N, max_pages, P)
+    _int32("lens", lens, (N,))
+    if out is not None:
+        _state("out.pages", out.pages, N, max_pages, P)
+        _check_out("status", out.status, torch.int32, (1,))
+    dev = _device_of(pages.table, lens=lens, **_state_tensors("pages", pages),
+                     **({} if out is None else dict(_state_tensors("out.pages", out.pages),
+                                                    status=out.status)))
+    if out is None:
+        out = ResizeResult(_like(pages), _new_status(dev))
+    st = psi_cache_resize(N, max_pages, P, page_size, _ptr(lens), extra, src,
+                          _state("out.pages", out.pages, N, max_pages, P), _ptr(out.status),
+                          _stream(stream))
+    _check(st, "psi_cache_resize")
+    return out
+
+
+def cache_fork(k_pages, v_pages, pages: PageState, lens, src, dst, workspace=None, stream=None,
+               out: ForkResult | None = None) -> ForkResult:
+    """Row dst[k] becomes a copy of row src[k] (``psi_cache_fork``): whole
+    pages are shared, the last, partly filled one is copied in every layer.
+
+    k_pages, v_pages [L, P, S, H, D]; src, dst int32 [K].  Returns a new
+    state and lengths; ``out`` may name the given ones (in place).
+    """
+    torch = _torch()
+    lay = _layout(k_pages, v_pages, layered=True)
+    if pages.table.dim() != 2 or src.dim() != 1:
+        raise ValueError("pages.table must be [N, max_pages], src and dst [K]")
+    N, max_pages = pages.table.shape
+    P, K = lay.num_pages, src.shape[0]
+    state = _state("pages", pages, N, max_pages, P)
+    _int32("lens", lens, (N,))
+    _int32("src", src, (K,))
+    _int32("dst", dst, (K,))
+    if out is not None:
+        _state("out.pages", out.pages, N, max_pages, P)
+        _check_out("lens", out.lens, torch.int32, (N,))
+        _check_out("status", out.status, torch.int32, (1,))
+    _check_workspace(workspace)
+    dev = _device_of(k_pages, v_pages=v_pages, lens=lens, src=src, dst=dst, workspace=workspace,
+                     **_state_tensors("pages", pages),
+                     **({} if out is None else dict(_state_tensors("out.pages", out.pages),
+                                                    out_lens=out.lens, status=out.status)))
+    if out is None:
+        out = ForkResult(_like(pages), torch.empty_like(lens), _new_status(dev))
+    ws_bytes = psi_cache_fork_workspace_bytes(K)
+    if ws_bytes and (workspace is None or _nbytes(workspace) < ws_bytes):
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    st = psi_cache_fork(lay, _ptr(k_pages), _ptr(v_pages), N, max_pages, _ptr(lens),
+                        _ptr(out.lens), state, _state("out.pages", out.pages, N, max_pages, P), K,
+                        _ptr(src), _ptr(dst), _ptr(out.status), _ptr(workspace),
+                        _nbytes(workspace), _stream(stream))
+    _check(st, "psi_cache_fork")
+    return out

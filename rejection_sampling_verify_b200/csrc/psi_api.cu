@@ -7,7 +7,7 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "psi_internal.h"
+#include "psi_cache.h"
 
 namespace psi {
 
@@ -68,6 +68,15 @@ int32_t max_v(psi_dtype dt) { return dt == PSI_DTYPE_F32 ? PSI_MAX_V / 2 : PSI_M
 bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 }  // namespace
+
+// The same error slot for the ABI's other translation units.
+psi_status psi::api_fail(psi_status st, const char *fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
+  va_end(ap);
+  return st;
+}
 
 extern "C" {
 

@@ -1,0 +1,312 @@
+// psi_attend.cu - attention of a drafted block over the paged cache.
+//
+// Row r of a sequence's block and query head h form one packed row; the
+// packed rows of one kv head share its keys and values.  A CTA takes a tile
+// of packed rows and one range of the sequence's positions, keeps a running
+// maximum and sum per row (online softmax) and, when the length is split,
+// leaves a partial result that join_kernel adds up.
+#include <math.h>
+
+#include <algorithm>
+
+#include "psi_cache.h"
+
+namespace psi {
+namespace {
+
+constexpr int kRowTile = 16;     // packed rows per CTA: four per warp
+constexpr int kTokTile = 32;     // positions per step: one per lane
+constexpr int kSimtThreads = 128;
+constexpr float kNegInf = -INFINITY;
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <typename Bits>
+struct Store;
+template <>
+struct Store<uint16_t> {
+  __device__ static void put(void *p, int64_t i, float v) {
+    static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16(v);
+  }
+};
+template <>
+struct Store<uint32_t> {
+  __device__ static void put(void *p, int64_t i, float v) { static_cast<float *>(p)[i] = v; }
+};
+
+// Eight elements (16-byte aligned) as floats.
+template <typename Bits>
+__device__ __forceinline__ void load8(const void *base, int64_t at, float f[8]) {
+  const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const Bits *>(base) + at);
+  if constexpr (sizeof(Bits) == 2) {
+    const uint4 v = *p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = Elem<Bits>::to_float(vec_elem<Bits>(v, i));
+  } else {
+    const uint4 v = p[0], w = p[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = Elem<Bits>::to_float(vec_elem<Bits>(v, i));
+      f[4 + i] = Elem<Bits>::to_float(vec_elem<Bits>(w, i));
+    }
+  }
+}
+
+__device__ __forceinline__ float4 lds4(const float *p) {
+  return *reinterpret_cast<const float4 *>(p);
+}
+
+// Any head size, both element types: products in float on the FMA pipe.
+template <typename Bits>
+__global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int32_t row_tiles) {
+  extern __shared__ __align__(16) float smem[];
+  const int D = a.D, G = a.q_heads / a.kv_heads, KS = D + 4;
+  float *qs = smem;                           // [kRowTile][D]
+  float *ks = qs + kRowTile * D;              // [kTokTile][D + 4]
+  float *vs = ks + kTokTile * KS;             // [kTokTile][D]
+  float *ps = vs + kTokTile * D;              // [4 warps][kTokTile][4 rows]
+  __shared__ uint32_t sees[kRowTile][kBlockWords];
+  __shared__ int64_t offs[kTokTile];
+
+  int64_t id = blockIdx.x;
+  const int split = (int)(id % a.splits);
+  id /= a.splits;
+  const int tile = (int)(id % row_tiles);
+  id /= row_tiles;
+  const int h = (int)(id % a.kv_heads);
+  const int n = (int)(id / a.kv_heads);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int len = a.g.lens[n];
+  if (len < 0) return;  // the sequence is not there
+  const int rows = a.R * G;
+  const int32_t *parents = a.parents ? a.parents + (int64_t)n * (a.R - 1) : nullptr;
+  const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
+  const int64_t cap = table_capacity(a.g);
+  const int64_t want = (int64_t)len + a.R;
+  const int T = (int)(want < cap ? want : cap);
+  if (want > cap && a.dev_status && tid == 0) atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
+
+  for (int i = tid; i < kRowTile; i += kSimtThreads) {
+    const int pr = tile * kRowTile + i;
+    uint32_t bits[kBlockWords] = {};
+    if (pr < rows && !row_sees(parents, pr / G, bits) && a.dev_status)
+      atomicOr(a.dev_status, PSI_DEV_BAD_PARENT);
+    for (int w = 0; w < kBlockWords; ++w) sees[i][w] = bits[w];
+  }
+  for (int i = tid; i < kRowTile * D / 8; i += kSimtThreads) {
+    const int r = i / (D / 8), c = i % (D / 8) * 8, pr = tile * kRowTile + r;
+    float f[8] = {};
+    if (pr < rows)
+      load8<Bits>(a.q,
+                  ((int64_t)n * a.R + pr / G) * a.q_row_stride +
+                      (int64_t)(h * G + pr % G) * a.q_head_stride + c,
+                  f);
+    for (int k = 0; k < 8; ++k) qs[r * D + c + k] = f[k] * a.scale2;
+  }
+  __syncthreads();
+
+  const int per = ((T + a.splits - 1) / a.splits + kTokTile - 1) / kTokTile * kTokTile;
+  const int begin = split * per < T ? split * per : T;
+  const int end = begin + per < T ? begin + per : T;
+  float m[4], l[4], acc[4][8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    m[i] = kNegInf;
+    l[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
+  }
+  // bit 0 of sees[][0] is the root: set for every row that belongs to the block
+  bool live[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) live[i] = sees[warp * 4 + i][0] & 1u;
+  const float *qrow = qs + warp * 4 * D;
+  float *prow = ps + warp * kTokTile * 4;
+
+  for (int t0 = begin; t0 < end; t0 += kTokTile) {
+    if (tid < kTokTile) {
+      const int t = t0 + tid;
+      const int64_t o = t < end ? slot_offset(a.g, table, t) : -1;
+      if (t < end && o < 0 && a.dev_status) atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
+      offs[tid] = o;
+    }
+    __syncthreads();
+    for (int i = tid; i < kTokTile * D / 8; i += kSimtThreads) {
+      const int t = i / (D / 8), c = i % (D / 8) * 8;
+      float fk[8] = {}, fv[8] = {};
+      if (offs[t] >= 0) {
+        const int64_t at = offs[t] + (int64_t)h * a.g.head_stride + c;
+        load8<Bits>(a.k, at, fk);
+        load8<Bits>(a.v, at, fv);
+      }
+      for (int k = 0; k < 8; ++k) {
+        ks[t * KS + c + k] = fk[k];
+        vs[t * D + c + k] = fv[k];
+      }
+    }
+    __syncthreads();
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int d = 0; d < D; d += 4) {
+      const float4 kk = lds4(ks + lane * KS + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 q4 = lds4(qrow + i * D + d);
+        s[i] = fmaf(q4.x, kk.x, fmaf(q4.y, kk.y, fmaf(q4.z, kk.z, fmaf(q4.w, kk.w, s[i]))));
+      }
+    }
+    const int t = t0 + lane, back = t - len;
+    const bool there = t < end && offs[lane] >= 0;
+    float scale[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool seen =
+          there && live[i] &&
+          (back < 0 || ((sees[warp * 4 + i][back >> 5] >> (back & 31)) & 1u));
+      const float x = seen ? s[i] : kNegInf;
+      const float top = fmaxf(m[i], warp_max(x));
+      // nothing seen so far: keep the weights at zero rather than inf - inf
+      const float ref = top == kNegInf ? 0.f : top;
+      const float p = seen ? fast_exp2(x - ref) : 0.f;
+      scale[i] = fast_exp2(m[i] - ref);
+      l[i] = l[i] * scale[i] + warp_sum(p);
+      m[i] = top;
+      prow[lane * 4 + i] = seen ? p : -1.f;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[i][k] *= scale[i];
+    const int last = end - t0 < kTokTile ? end - t0 : kTokTile;
+    for (int j = 0; j < last; ++j) {
+      const float4 p4 = lds4(prow + j * 4);
+      const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int d = lane * 4 + c * 128;
+        if (d >= D) continue;
+        const float4 v4 = lds4(vs + j * D + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (p[i] < 0.f) continue;  // not seen: it may be inf or NaN
+          acc[i][c * 4 + 0] = fmaf(p[i], v4.x, acc[i][c * 4 + 0]);
+          acc[i][c * 4 + 1] = fmaf(p[i], v4.y, acc[i][c * 4 + 1]);
+          acc[i][c * 4 + 2] = fmaf(p[i], v4.z, acc[i][c * 4 + 2]);
+          acc[i][c * 4 + 3] = fmaf(p[i], v4.w, acc[i][c * 4 + 3]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pr = tile * kRowTile + warp * 4 + i;
+    if (pr >= rows) continue;
+    const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
+    if (a.splits > 1) {
+      const int64_t at = row * a.splits + split;
+      if (lane == 0) a.part_ml[at] = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int d = lane * 4 + c * 128;
+        if (d < D)
+          *reinterpret_cast<float4 *>(a.part_o + at * D + d) =
+              make_float4(acc[i][c * 4], acc[i][c * 4 + 1], acc[i][c * 4 + 2], acc[i][c * 4 + 3]);
+      }
+    } else {
+      const bool any = l[i] != 0.f;  // (true for NaN)
+      const float inv = any ? 1.f / l[i] : 0.f;
+      if (lane == 0 && a.out_lse) a.out_lse[row] = any ? m[i] * kLn2 + logf(l[i]) : kNegInf;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int d = lane * 4 + k / 4 * 128 + k % 4;
+        if (d < D)
+          Store<Bits>::put(a.out_o, row * D + d, any ? acc[i][k] * inv : 0.f);
+      }
+    }
+  }
+}
+
+// Adds up the partial results of one output row, in the order of the splits:
+// one warp per row.
+template <typename Bits>
+__global__ void __launch_bounds__(128) join_kernel(AttendArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (row >= (int64_t)a.N * a.R * a.q_heads) return;
+  if (a.g.lens[row / ((int64_t)a.R * a.q_heads)] < 0) return;
+  const float2 *ml = a.part_ml + row * a.splits;
+  float top = kNegInf;
+  bool any = false;
+  for (int s = 0; s < a.splits; ++s) {
+    top = fmaxf(top, ml[s].x);
+    any |= ml[s].y != 0.f;
+  }
+  float l = 0.f, acc[8] = {};
+  for (int s = 0; any && s < a.splits; ++s) {
+    if (ml[s].y == 0.f) continue;
+    const float w = fast_exp2(ml[s].x - top);
+    l = fmaf(w, ml[s].y, l);
+    const float *o = a.part_o + (row * a.splits + s) * a.D;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k * 32 + lane < a.D) acc[k] = fmaf(w, o[k * 32 + lane], acc[k]);
+  }
+  if (lane == 0 && a.out_lse)
+    a.out_lse[row] = any ? top * kLn2 + logf(l) : kNegInf;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k * 32 + lane < a.D)
+      Store<Bits>::put(a.out_o, row * a.D + k * 32 + lane, any ? acc[k] / l : 0.f);
+}
+
+size_t simt_smem(int D) {
+  return sizeof(float) *
+         ((size_t)kRowTile * D + (size_t)kTokTile * (D + 4) + (size_t)kTokTile * D + 4 * kTokTile * 4);
+}
+
+template <typename Bits>
+cudaError_t launch_typed(const AttendArgs &a, const AttendPlan &plan, cudaStream_t stream) {
+  static DeviceOnce once;
+  cudaError_t e = once([] {
+    return cudaFuncSetAttribute(attend_kernel<Bits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)simt_smem(PSI_MAX_HEAD_DIM));
+  });
+  if (e != cudaSuccess) return e;
+  attend_kernel<Bits><<<(unsigned)plan.ctas, kSimtThreads, simt_smem(a.D), stream>>>(
+      a, plan.row_tiles);
+  if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+  const int64_t rows = (int64_t)a.N * a.R * a.q_heads;
+  join_kernel<Bits><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, int32_t D,
+                       psi_dtype dtype, int64_t capacity) {
+  (void)dtype;
+  AttendPlan p;
+  p.row_tiles = (R * (q_heads / kv_heads) + kRowTile - 1) / kRowTile;
+  const int64_t base = (int64_t)N * kv_heads * p.row_tiles;
+  const int64_t fill = (int64_t)device_sm_count() * 4;
+  const int64_t most = std::max<int64_t>(1, capacity / 256);
+  p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({(fill + base - 1) / base, most, 128}));
+  p.ctas = base * p.splits;
+  const size_t parts = (size_t)N * R * q_heads * p.splits;
+  p.workspace = p.splits > 1 ? parts * (sizeof(float) * D + sizeof(float2)) : 0;
+  return p;
+}
+
+cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan, void *workspace,
+                          cudaStream_t stream) {
+  a.splits = plan.splits;
+  if (plan.ctas > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
+  const size_t parts = (size_t)a.N * a.R * a.q_heads * plan.splits;
+  a.part_o = static_cast<float *>(workspace);
+  a.part_ml = reinterpret_cast<float2 *>(a.part_o + parts * a.D);
+  return dtype == PSI_DTYPE_BF16 ? launch_typed<uint16_t>(a, plan, stream)
+                                 : launch_typed<uint32_t>(a, plan, stream);
+}
+
+}  // namespace psi

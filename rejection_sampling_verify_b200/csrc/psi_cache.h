@@ -1,0 +1,99 @@
+// psi_cache.h - launchers of the key-value cache kernels.  Not part of the
+// public ABI.
+#pragma once
+
+#include "psi_internal.h"
+#include "psi_paging.h"
+
+namespace psi {
+
+// A block's queries against one layer's pages.
+struct AttendArgs {
+  Paging g;
+  const void *k, *v;  // pools
+  const void *q;
+  int64_t q_row_stride, q_head_stride;
+  int32_t N, R, q_heads, kv_heads, D;
+  const int32_t *parents;  // [N][R - 1] or nullptr
+  float scale2;            // scale * log2(e): scores are taken in powers of two
+  void *out_o;
+  float *out_lse;
+  uint32_t *dev_status;
+  // split over the length: partial results, joined by a second kernel
+  int32_t splits;
+  float *part_o;   // [N * R * q_heads][splits][D], relative to part_ml's maximum
+  float2 *part_ml; // [N * R * q_heads][splits]: maximum (log2 units), sum
+};
+struct AttendPlan {
+  int32_t splits, row_tiles;
+  int64_t ctas;
+  size_t workspace;
+};
+AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, int32_t D,
+                       psi_dtype dtype, int64_t capacity);
+cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan, void *workspace,
+                          cudaStream_t stream);
+
+struct AppendArgs {
+  Paging g;
+  void *k_pool, *v_pool;
+  const void *q, *k, *v;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;  // strides in elements
+  int32_t N, R, q_heads, kv_heads, D;
+  const void *q_weight, *k_weight;
+  float eps;
+  const double *inv_freq;
+  int32_t rotary_dim, interleaved;
+  float rope_scale;
+  const int32_t *parents;
+  void *out_q;
+  uint32_t *dev_status;
+};
+cudaError_t launch_append(const AppendArgs &a, psi_dtype dtype, cudaStream_t stream);
+
+struct CommitArgs {
+  Paging g;
+  void *k_pool, *v_pool;
+  int32_t layers;
+  int64_t layer_bytes, page_bytes, slot_bytes, head_bytes;
+  int32_t kv_heads, head_vecs;  // 16-byte vectors per head
+  int32_t N, M;
+  const int32_t *path_nodes, *path_len;
+  int32_t *out_lens;
+  uint32_t *dev_status;
+};
+cudaError_t launch_commit(const CommitArgs &a, cudaStream_t stream);
+
+struct ResizeArgs {
+  int32_t N, max_pages, num_pages, page_size;
+  const int32_t *lens;
+  int32_t extra;
+  psi_page_state in, out;
+  uint32_t *dev_status;
+};
+cudaError_t launch_resize(const ResizeArgs &a, cudaStream_t stream);
+
+// One page to copy: `count` slots of page `from` to page `to`.
+struct PageCopy {
+  int32_t from, to, count;
+};
+struct ForkArgs {
+  int32_t N, max_pages, num_pages, page_size;
+  const int32_t *lens;
+  int32_t *out_lens;
+  psi_page_state in, out;
+  int32_t K;
+  const int32_t *src, *dst;
+  PageCopy *copies;  // [K]
+  uint32_t *dev_status;
+  // the pools
+  void *k_pool, *v_pool;
+  int32_t layers, kv_heads, head_vecs;
+  int64_t layer_bytes, page_bytes, slot_bytes, head_bytes;
+};
+cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream);
+
+// Host-side error reporting of the C ABI (psi_api.cu).
+psi_status api_fail(psi_status st, const char *fmt, ...);
+
+}  // namespace psi

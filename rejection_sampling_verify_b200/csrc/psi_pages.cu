@@ -1,0 +1,342 @@
+// psi_pages.cu - the pages of the key-value cache: moving an accepted path
+// behind its prefix, fitting a sequence's pages to its length, and forking.
+#include "psi_cache.h"
+
+namespace psi {
+namespace {
+
+// ---- commit --------------------------------------------------------------------
+// One CTA per (sequence, layer, pool).  Every 16-byte column of a slot is one
+// thread's: it loads a batch of accepted nodes' columns and stores them in
+// order.  A node never moves to a later slot and the path ascends, so a
+// store never lands on a column that this thread has yet to load.
+constexpr int kCommitThreads = 128;
+constexpr int kCommitBatch = 8;
+
+__global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a) {
+  const int n = blockIdx.x, layer = blockIdx.y, pool = blockIdx.z;
+  const int len = a.g.lens[n];
+  if (len < 0) {
+    if (layer == 0 && pool == 0 && threadIdx.x == 0) a.out_lens[n] = len;
+    return;
+  }
+  const int32_t *nodes = a.path_nodes + (int64_t)n * a.M;
+  const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
+  const int want = a.path_len[n];
+  const int keep = path_prefix(nodes, want, a.M);
+  if (layer == 0 && pool == 0 && threadIdx.x == 0) {
+    const int64_t now = (int64_t)len + 1 + keep;
+    a.out_lens[n] = now > INT32_MAX ? INT32_MAX : (int32_t)now;
+    if (keep != want && a.dev_status) atomicOr(a.dev_status, PSI_DEV_BAD_PATH);
+  }
+  char *base = static_cast<char *>(pool ? a.v_pool : a.k_pool) + layer * a.layer_bytes;
+  for (int col = threadIdx.x; col < a.kv_heads * a.head_vecs; col += kCommitThreads) {
+    char *at = base + (col / a.head_vecs) * a.head_bytes + (col % a.head_vecs) * 16;
+    for (int j0 = 0; j0 < keep; j0 += kCommitBatch) {
+      uint4 x[kCommitBatch];
+#pragma unroll
+      for (int j = 0; j < kCommitBatch; ++j) {
+        if (j0 + j >= keep || nodes[j0 + j] == j0 + j) continue;
+        const int64_t t = (int64_t)len + 1 + nodes[j0 + j];
+        const int32_t p = page_of(a.g, table, t);
+        if (p >= 0)
+          x[j] = *reinterpret_cast<const uint4 *>(at + p * a.page_bytes +
+                                                  (t % a.g.page_size) * a.slot_bytes);
+        else if (a.dev_status)
+          atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
+      }
+#pragma unroll
+      for (int j = 0; j < kCommitBatch; ++j) {
+        if (j0 + j >= keep || nodes[j0 + j] == j0 + j) continue;
+        const int64_t t = (int64_t)len + 1 + j0 + j;
+        const int32_t p = page_of(a.g, table, t);
+        if (p >= 0 && page_of(a.g, table, (int64_t)len + 1 + nodes[j0 + j]) >= 0)
+          *reinterpret_cast<uint4 *>(at + p * a.page_bytes + (t % a.g.page_size) * a.slot_bytes) =
+              x[j];
+        else if (a.dev_status)
+          atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
+      }
+    }
+  }
+}
+
+// ---- page bookkeeping ----------------------------------------------------------------
+constexpr int kPageThreads = 1024;
+
+// Exclusive sum over the CTA; *total gets the sum of all.
+__device__ int64_t block_scan(int64_t v, int64_t *total) {
+  __shared__ int64_t warps[kPageThreads / 32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int64_t x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, w, o);
+      if (lane >= o) w += y;
+    }
+    warps[lane] = w;
+  }
+  __syncthreads();
+  const int64_t before = warp ? warps[warp - 1] : 0;
+  *total = warps[kPageThreads / 32 - 1];
+  __syncthreads();
+  return before + x - v;
+}
+
+// Carries `count` words over where the two arrays differ.
+__device__ void carry(const int32_t *from, int32_t *to, int64_t count) {
+  if (from == to) return;
+  for (int64_t i = threadIdx.x; i < count; i += kPageThreads) to[i] = from[i];
+}
+
+__device__ int stack_height(const int32_t *n_free, int num_pages, uint32_t *dev_status) {
+  int n = *n_free;
+  if (n < 0 || n > num_pages) {
+    if (threadIdx.x == 0 && dev_status) atomicOr(dev_status, PSI_DEV_BAD_PAGE);
+    n = n < 0 ? 0 : num_pages;
+  }
+  return n;
+}
+
+// A page whose last holder let it go in this call is marked until the stack
+// takes it: an erroneous second release of it then shows.
+constexpr int32_t kGone = -(1 << 30);
+
+__global__ void __launch_bounds__(kPageThreads) resize_kernel(ResizeArgs a) {
+  const int tid = threadIdx.x;
+  const auto flag = [&](uint32_t bit) {
+    if (a.dev_status) atomicOr(a.dev_status, bit);
+  };
+  carry(a.in.page_table, a.out.page_table, (int64_t)a.N * a.max_pages);
+  carry(a.in.page_counts, a.out.page_counts, a.N);
+  carry(a.in.refs, a.out.refs, a.num_pages);
+  carry(a.in.free_pages, a.out.free_pages, a.num_pages);
+  int height = stack_height(a.in.n_free, a.num_pages, a.dev_status);
+  __syncthreads();
+
+  // release what is over: a warp per sequence
+  for (int n = tid / 32; n < a.N; n += kPageThreads / 32) {
+    const int len = a.lens[n];
+    if (len < 0) continue;
+    int held = a.out.page_counts[n];
+    if (held < 0 || held > a.max_pages) {
+      flag(PSI_DEV_BAD_PAGE);
+      held = held < 0 ? 0 : a.max_pages;
+    }
+    const int64_t need = pages_for((int64_t)len + a.extra, a.page_size);
+    int32_t *row = a.out.page_table + (int64_t)n * a.max_pages;
+    for (int64_t i = need + tid % 32; i < held; i += 32) {
+      const int32_t p = row[i];
+      row[i] = -1;
+      if (p < 0 || p >= a.num_pages) {
+        flag(PSI_DEV_BAD_PAGE);
+        continue;
+      }
+      const int32_t before = atomicSub(a.out.refs + p, 1);
+      if (before == 1)
+        atomicAdd(a.out.refs + p, kGone);
+      else if (before < 1)
+        flag(PSI_DEV_BAD_PAGE);
+    }
+    __syncwarp();
+    if (tid % 32 == 0 && need < held) a.out.page_counts[n] = (int32_t)need;
+    else if (tid % 32 == 0) a.out.page_counts[n] = held;
+  }
+  __syncthreads();
+
+  // push what nobody holds any more, lowest page first: a range per thread
+  const int per = (a.num_pages + kPageThreads - 1) / kPageThreads;
+  const int64_t p0 = (int64_t)tid * per;
+  const int64_t p1 = p0 + per < a.num_pages ? p0 + per : a.num_pages;
+  int64_t mine = 0, total;
+  for (int64_t p = p0; p < p1; ++p) mine += a.out.refs[p] <= kGone / 2;
+  int64_t at = height + block_scan(mine, &total);
+  for (int64_t p = p0; p < p1; ++p) {
+    const int32_t refs = a.out.refs[p];
+    if (refs <= kGone / 2) {
+      if (at < a.num_pages) a.out.free_pages[at] = (int32_t)p;
+      else flag(PSI_DEV_BAD_PAGE);
+      ++at;
+    }
+    if (refs < 0) a.out.refs[p] = 0;
+  }
+  height = height + total < a.num_pages ? (int)(height + total) : a.num_pages;
+  __syncthreads();
+
+  // pop what is missing, in the order of the sequences: all that a sequence
+  // needs, or none
+  __shared__ int64_t first[kPageThreads];
+  __shared__ int32_t count[kPageThreads];
+  int64_t asked = 0, given = 0;
+  for (int n0 = 0; n0 < a.N; n0 += kPageThreads) {
+    const int n = n0 + tid;
+    int held = 0;
+    int64_t want = 0, sum;
+    if (n < a.N && a.lens[n] >= 0) {
+      held = a.out.page_counts[n];
+      const int64_t need = pages_for((int64_t)a.lens[n] + a.extra, a.page_size);
+      if (need > a.max_pages)
+        flag(PSI_DEV_NO_PAGES);
+      else if (need > held)
+        want = need - held;
+    }
+    const int64_t before = asked + block_scan(want, &sum);
+    asked += sum;
+    const bool fits = before + want <= height;
+    if (want && !fits) flag(PSI_DEV_NO_PAGES);
+    first[tid] = before;
+    count[tid] = fits ? (int32_t)want : 0;
+    block_scan(count[tid], &sum);  // (and every thread's first and count are there)
+    given += sum;
+    const int here = a.N - n0 < kPageThreads ? a.N - n0 : kPageThreads;
+    for (int i = tid / 32; i < here; i += kPageThreads / 32) {
+      if (!count[i]) continue;
+      const int base = a.out.page_counts[n0 + i];
+      int32_t *row = a.out.page_table + (int64_t)(n0 + i) * a.max_pages + base;
+      for (int j = tid % 32; j < count[i]; j += 32) {
+        int32_t p = a.out.free_pages[height - 1 - (first[i] + j)];
+        if (p < 0 || p >= a.num_pages || atomicExch(a.out.refs + p, 1) != 0) {
+          flag(PSI_DEV_BAD_PAGE);  // not a free page
+          if (p < 0 || p >= a.num_pages) p = -1;
+        }
+        row[j] = p;
+      }
+      __syncwarp();
+      if (tid % 32 == 0) a.out.page_counts[n0 + i] = base + count[i];
+    }
+    __syncthreads();
+  }
+  if (tid == 0) *a.out.n_free = height - (int)given;
+}
+
+// ---- fork ------------------------------------------------------------------------
+__global__ void __launch_bounds__(kPageThreads) fork_kernel(ForkArgs a) {
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const auto flag = [&](uint32_t bit) {
+    if (a.dev_status) atomicOr(a.dev_status, bit);
+  };
+  // which forks can be made, from the state before the call: a warp per fork
+  for (int k = warp; k < a.K; k += kPageThreads / 32) {
+    const int src = a.src[k], dst = a.dst[k];
+    bool ok = src >= 0 && src < a.N && dst >= 0 && dst < a.N;
+    for (int j = lane; ok && j < a.K; j += 32)
+      ok = a.src[j] != dst && (j >= k || a.dst[j] != dst);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    int len = 0;
+    if (ok) {
+      len = a.lens[src];
+      ok = len >= 0 && a.in.page_counts[dst] == 0;
+    }
+    const bool named = ok;
+    if (ok) {
+      const int64_t need = pages_for(len, a.page_size);
+      ok = need <= a.in.page_counts[src] && need <= a.max_pages;
+      const int32_t *row = a.in.page_table + (int64_t)src * a.max_pages;
+      for (int64_t i = lane; ok && i < need; i += 32) ok = row[i] >= 0 && row[i] < a.num_pages;
+      ok = __all_sync(0xFFFFFFFFu, ok);
+    }
+    if (lane == 0) {
+      if (!ok) flag(named ? PSI_DEV_BAD_PAGE : PSI_DEV_BAD_SEQ);
+      const int whole = len / a.page_size;
+      a.copies[k].count = ok ? len % a.page_size : -1;
+      a.copies[k].from =
+          ok && len % a.page_size ? a.in.page_table[(int64_t)src * a.max_pages + whole] : -1;
+    }
+  }
+  const int height = stack_height(a.in.n_free, a.num_pages, a.dev_status);
+  __syncthreads();
+  carry(a.in.page_table, a.out.page_table, (int64_t)a.N * a.max_pages);
+  carry(a.in.page_counts, a.out.page_counts, a.N);
+  carry(a.in.refs, a.out.refs, a.num_pages);
+  carry(a.in.free_pages, a.out.free_pages, a.num_pages);
+  carry(a.lens, a.out_lens, a.N);
+  __syncthreads();
+
+  // a page for each length that ends inside one, in the order of the forks
+  int64_t asked = 0, given = 0;
+  for (int k0 = 0; k0 < a.K; k0 += kPageThreads) {
+    const int k = k0 + tid;
+    const bool needs = k < a.K && a.copies[k].count > 0;
+    int64_t sum;
+    const int64_t at = asked + block_scan(needs, &sum);
+    asked += sum;
+    int32_t p = -1;
+    if (needs) {
+      if (at < height) p = a.out.free_pages[height - 1 - at];
+      if (at >= height) flag(PSI_DEV_NO_PAGES);
+      else if (p < 0 || p >= a.num_pages || atomicExch(a.out.refs + p, 1) != 0) {
+        flag(PSI_DEV_BAD_PAGE);
+        p = -1;
+      }
+      a.copies[k].to = p;
+      if (p < 0) a.copies[k].count = -1;
+    }
+  }
+  given = asked < height ? asked : height;
+  __syncthreads();
+  for (int k = warp; k < a.K; k += kPageThreads / 32) {
+    const PageCopy c = a.copies[k];
+    if (c.count < 0) continue;
+    const int src = a.src[k], dst = a.dst[k], len = a.lens[src];
+    const int whole = len / a.page_size;
+    const int32_t *from = a.out.page_table + (int64_t)src * a.max_pages;
+    int32_t *row = a.out.page_table + (int64_t)dst * a.max_pages;
+    for (int i = lane; i < whole; i += 32) {
+      row[i] = from[i];
+      atomicAdd(a.out.refs + from[i], 1);
+    }
+    if (lane == 0) {
+      if (c.count > 0) row[whole] = c.to;
+      a.out.page_counts[dst] = whole + (c.count > 0);
+      a.out_lens[dst] = len;
+    }
+  }
+  if (tid == 0) *a.out.n_free = height - (int)given;
+}
+
+// The partial pages' filled slots, one CTA per (fork, layer, pool).
+constexpr int kCopyThreads = 256;
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(ForkArgs a) {
+  const PageCopy c = a.copies[blockIdx.x];
+  if (c.count <= 0) return;
+  char *base = static_cast<char *>(blockIdx.z ? a.v_pool : a.k_pool) + blockIdx.y * a.layer_bytes;
+  const int per_slot = a.kv_heads * a.head_vecs;
+  for (int i = threadIdx.x; i < c.count * per_slot; i += kCopyThreads) {
+    const int col = i % per_slot;
+    const int64_t at = (i / per_slot) * a.slot_bytes + (col / a.head_vecs) * a.head_bytes +
+                       (col % a.head_vecs) * 16;
+    *reinterpret_cast<uint4 *>(base + c.to * a.page_bytes + at) =
+        *reinterpret_cast<const uint4 *>(base + c.from * a.page_bytes + at);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_commit(const CommitArgs &a, cudaStream_t stream) {
+  commit_kernel<<<dim3(a.N, a.layers, 2), kCommitThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_resize(const ResizeArgs &a, cudaStream_t stream) {
+  resize_kernel<<<1, kPageThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fork(const ForkArgs &a, cudaStream_t stream) {
+  fork_kernel<<<1, kPageThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  page_copy_kernel<<<dim3(a.K, a.layers, 2), kCopyThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace psi
