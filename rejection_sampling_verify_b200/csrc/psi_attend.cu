@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   const int h = (int)(id % a.kv_heads);
   const int n = (int)(id / a.kv_heads);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  pdl_wait();
   const int len = a.g.lens[n];
   if (len < 0) return;  // the sequence is not there
   const int rows = a.R * G;
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(128) join_kernel(AttendArgs a) {
   const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
   if (row >= (int64_t)a.N * a.R * a.q_heads) return;
+  pdl_wait();
   if (a.g.lens[row / ((int64_t)a.R * a.q_heads)] < 0) return;
   const float2 *ml = a.part_ml + row * a.splits;
   float top = kNegInf;
@@ -266,32 +268,37 @@ size_t simt_smem(int D) {
 }
 
 template <typename Bits>
-cudaError_t launch_typed(const AttendArgs &a, const AttendPlan &plan, cudaStream_t stream) {
+cudaError_t launch_simt(const AttendArgs &a, const AttendPlan &plan, cudaStream_t stream) {
   static DeviceOnce once;
-  cudaError_t e = once([] {
+  const cudaError_t e = once([] {
     return cudaFuncSetAttribute(attend_kernel<Bits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)simt_smem(PSI_MAX_HEAD_DIM));
   });
   if (e != cudaSuccess) return e;
-  attend_kernel<Bits><<<(unsigned)plan.ctas, kSimtThreads, simt_smem(a.D), stream>>>(
-      a, plan.row_tiles);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+  return launch_pdl(attend_kernel<Bits>, dim3((unsigned)plan.ctas), dim3(kSimtThreads),
+                    simt_smem(a.D), stream, a, plan.row_tiles);
+}
+
+template <typename Bits>
+cudaError_t launch_join(const AttendArgs &a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.N * a.R * a.q_heads;
-  join_kernel<Bits><<<(unsigned)((rows + 3) / 4), 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(join_kernel<Bits>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a);
 }
 
 }  // namespace
 
 AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, int32_t D,
                        psi_dtype dtype, int64_t capacity) {
-  (void)dtype;
   AttendPlan p;
-  p.row_tiles = (R * (q_heads / kv_heads) + kRowTile - 1) / kRowTile;
+  const int rows = R * (q_heads / kv_heads);
+  p.tc = attend_tc_fits(dtype, D);
+  p.rows = p.tc ? attend_tc_rows(rows) : kRowTile;
+  p.row_tiles = (rows + p.rows - 1) / p.rows;
   const int64_t base = (int64_t)N * kv_heads * p.row_tiles;
-  const int64_t fill = (int64_t)device_sm_count() * 4;
+  // CTAs that the device holds at once; a range is worth a CTA from 256 positions
+  const int64_t fill = (int64_t)device_sm_count() * (p.tc ? 2 : 4);
   const int64_t most = std::max<int64_t>(1, capacity / 256);
-  p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({(fill + base - 1) / base, most, 128}));
+  p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({fill / base, most, 128}));
   p.ctas = base * p.splits;
   const size_t parts = (size_t)N * R * q_heads * p.splits;
   p.workspace = p.splits > 1 ? parts * (sizeof(float) * D + sizeof(float2)) : 0;
@@ -305,8 +312,12 @@ cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan,
   const size_t parts = (size_t)a.N * a.R * a.q_heads * plan.splits;
   a.part_o = static_cast<float *>(workspace);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + parts * a.D);
-  return dtype == PSI_DTYPE_BF16 ? launch_typed<uint16_t>(a, plan, stream)
-                                 : launch_typed<uint32_t>(a, plan, stream);
+  const bool bf16 = dtype == PSI_DTYPE_BF16;
+  const cudaError_t e = plan.tc ? launch_attend_tc(a, plan, stream)
+                        : bf16  ? launch_simt<uint16_t>(a, plan, stream)
+                                : launch_simt<uint32_t>(a, plan, stream);
+  if (e != cudaSuccess || a.splits == 1) return e;
+  return bf16 ? launch_join<uint16_t>(a, stream) : launch_join<uint32_t>(a, stream);
 }
 
 }  // namespace psi

@@ -25,6 +25,8 @@ struct AttendArgs {
   float2 *part_ml; // [N * R * q_heads][splits]: maximum (log2 units), sum
 };
 struct AttendPlan {
+  bool tc;        // on the tensor cores
+  int32_t rows;   // packed rows per CTA
   int32_t splits, row_tiles;
   int64_t ctas;
   size_t workspace;
@@ -33,6 +35,11 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
                        psi_dtype dtype, int64_t capacity);
 cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan, void *workspace,
                           cudaStream_t stream);
+
+// The tensor-core form (psi_attend_tc.cu).
+bool attend_tc_fits(psi_dtype dtype, int32_t D);
+int attend_tc_rows(int rows);
+cudaError_t launch_attend_tc(const AttendArgs &a, const AttendPlan &plan, cudaStream_t stream);
 
 struct AppendArgs {
   Paging g;

@@ -1,0 +1,144 @@
+// psi_tcgen05.cuh - device building blocks of the tensor-core kernels
+// (sm_100a): tensor memory, tcgen05 matrix products on shared-memory
+// operands, asynchronous copies with an mbarrier arrival, and the bounded
+// waits between the warps of a CTA.
+#pragma once
+
+#include "psi_device.cuh"
+
+namespace psi {
+
+// ---- tensor memory -------------------------------------------------------------
+// One warp allocates and frees; `cols` is a power of two of at least 32.
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(slot)),
+               "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
+               : "memory");
+}
+
+// 16 columns of this warp's 32 lanes: r[c] is the thread's lane, column c.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float r[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+        "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+        "=f"(r[14]), "=f"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const float r[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"f"(r[0]),
+      "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]),
+      "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// Shared-memory accesses of this thread (and those it has waited for) before,
+// tensor-core reads after.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ---- matrix products -----------------------------------------------------------
+// Shared-memory operand: start address, the two strides in bytes, and the
+// layout (0: 8-row x 16-byte blocks, 2: 128-byte swizzle).
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride,
+                                            uint32_t layout) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(leading >> 4) << 16) |
+         ((uint64_t)(stride >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)layout << 61);
+}
+
+// bf16 x bf16 into float, 128 x n; a_mn, b_mn: the operand's rows (rather
+// than the summed index) are contiguous.
+constexpr uint32_t product_shape(int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n / 8) << 17) | ((128u / 16) << 24);
+}
+
+__device__ __forceinline__ void tc_product(uint32_t d, uint64_t a, uint64_t b, uint32_t shape,
+                                           bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
+      : "memory");
+}
+
+// Arrive on `bar` once all of this thread's products so far are done.
+__device__ __forceinline__ void tc_commit(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+
+// ---- asynchronous copies ---------------------------------------------------------
+// 16 bytes, or 16 zeros where `there` is false (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16u : 0u)
+               : "memory");
+}
+// Arrive (one of the barrier's expected arrivals) once this thread's copies
+// so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// ---- waits --------------------------------------------------------------------------
+// Waits for a phase unless the CTA gave up already; gives up after ~2 s and
+// tells the rest of the CTA.
+__device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity,
+                                                volatile uint32_t *gave_up) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*gave_up) return false;
+    if (global_timer_ns() - t0 > 2000000000ull) {
+      *gave_up = 1;
+      return false;
+    }
+  }
+}
+
+// Barrier of `threads` threads of the CTA, and the OR of their predicates.
+__device__ __forceinline__ bool named_or(int id, int threads, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)p), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0u;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+}  // namespace psi
