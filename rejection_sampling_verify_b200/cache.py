@@ -16,12 +16,13 @@ them on the current stream.  The order of a serving step is
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 from dataclasses import dataclass
 
 from . import (PSI_OK, PsiError, _check_out, _check_workspace, _device_of, _dtype_code, _nbytes,
-               _ptr, _stream, _torch, load_library)
+               _ptr, _torch, load_library)
 
 
 class CacheLayout(C.Structure):
@@ -225,9 +226,62 @@ def _block(q, page_table, lens, parents):
     return N, R
 
 
-def _new_status(dev):
+# A call's shapes, strides and dtypes decide what it may do: they are checked
+# once, and what was found (the layout, the strides, the workspace's size) is
+# kept under them.
+_MAX_PLANS = 512
+_plans = {}
+
+
+def _remember(key, plan):
+    if len(_plans) >= _MAX_PLANS:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype)
+
+
+def _on_device(ref, named):
+    """Index of the device of `ref`, which must be the current one and that of
+    the other tensors (``_device_of`` says what is wrong)."""
     torch = _torch()
-    return torch.zeros(1, dtype=torch.int32, device=dev)
+    dev = ref.get_device()
+    same = dev >= 0 and dev == torch._C._cuda_getDevice()
+    for t in named.values():
+        if t is not None and t.get_device() != dev:
+            same = False
+    if not same:
+        _device_of(ref, **named)
+    return dev
+
+
+# Status words, zeroed many at a time: each is handed out once.
+_STATUS_WORDS = 256
+_status_words = {}
+
+
+def _new_status(dev: int, stream: int):
+    """A zeroed status word for a call on `stream` (a raw handle) of `dev`."""
+    torch = _torch()
+    if torch.cuda.is_current_stream_capturing() or \
+            stream != torch._C._cuda_getCurrentRawStream(dev):
+        # (zeroed by the graph on every replay; or on the stream that the call names)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)) \
+                if stream != torch._C._cuda_getCurrentRawStream(dev) \
+                else contextlib.nullcontext():
+            return torch.zeros(1, dtype=torch.int32, device=dev)
+    words = _status_words.get((dev, stream))
+    if not words:
+        words = list(torch.zeros(_STATUS_WORDS, dtype=torch.int32, device=dev).split(1))
+        _status_words[dev, stream] = words
+    return words.pop()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def rope_frequencies(rotary_dim: int, theta: float = 1e6, factor: float = 1.0,
@@ -279,6 +333,35 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight=None, k_w
     inv_freq float64 [rotary_dim / 2] or None; parents int32 [N, R - 1] or
     None (a chain).  ``out.q`` may be ``q`` itself.
     """
+    key = ("append", _sig(q), _sig(k), _sig(v), _sig(k_pages), _sig(v_pages), _sig(page_table),
+           _sig(lens), _sig(q_weight), _sig(k_weight), _sig(inv_freq), _sig(parents))
+    plan = _plans.get(key) or _remember(key, _plan_append(
+        q, k, v, k_pages, v_pages, page_table, lens, q_weight, k_weight, inv_freq, parents))
+    lay, N, R, Hq, strides, rot, max_pages = plan
+    others = dict(k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table, lens=lens,
+                  q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq, parents=parents)
+    if out is not None:
+        torch = _torch()
+        _check_out("q", out.q, q.dtype, q.shape)
+        _check_out("status", out.status, torch.int32, (1,))
+        others.update(out_q=out.q, status=out.status)
+    dev = _on_device(q, others)
+    raw = _raw_stream(stream, dev)
+    if out is None:
+        out = AppendResult(_torch().empty(q.shape, dtype=q.dtype, device=q.device),
+                           _new_status(dev, raw))
+    st = psi_cache_append(
+        lay, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), max_pages,
+        lens.data_ptr(), N, R, Hq, q.data_ptr(), *strides[0], k.data_ptr(), *strides[1],
+        v.data_ptr(), *strides[2], _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq), rot,
+        1 if interleaved else 0, rope_scale, _ptr(parents), out.q.data_ptr(),
+        out.status.data_ptr(), raw)
+    _check(st, "psi_cache_append")
+    return out
+
+
+def _plan_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight, k_weight, inv_freq,
+                 parents):
     torch = _torch()
     N, R = _block(q, page_table, lens, parents)
     lay = _layout(k_pages, v_pages, layered=False)
@@ -292,23 +375,8 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight=None, k_w
     if inv_freq is not None and (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or
                                  not inv_freq.is_contiguous()):
         raise ValueError("inv_freq must be a contiguous float64 vector")
-    if out is not None:
-        _check_out("q", out.q, q.dtype, (N, R, Hq, D))
-        _check_out("status", out.status, torch.int32, (1,))
-    dev = _device_of(q, k=k, v=v, k_pages=k_pages, v_pages=v_pages, page_table=page_table,
-                     lens=lens, q_weight=q_weight, k_weight=k_weight, inv_freq=inv_freq,
-                     parents=parents,
-                     **({} if out is None else dict(out_q=out.q, status=out.status)))
-    if out is None:
-        out = AppendResult(torch.empty(N, R, Hq, D, dtype=q.dtype, device=dev), _new_status(dev))
-    st = psi_cache_append(
-        lay, _ptr(k_pages), _ptr(v_pages), _ptr(page_table), page_table.shape[1], _ptr(lens), N, R,
-        Hq, _ptr(q), *strides[0], _ptr(k), *strides[1], _ptr(v), *strides[2], _ptr(q_weight),
-        _ptr(k_weight), float(eps), _ptr(inv_freq), 0 if inv_freq is None else 2 * len(inv_freq),
-        int(bool(interleaved)), float(rope_scale), _ptr(parents), _ptr(out.q), _ptr(out.status),
-        _stream(stream))
-    _check(st, "psi_cache_append")
-    return out
+    return lay, N, R, Hq, strides, 0 if inv_freq is None else 2 * len(inv_freq), \
+        page_table.shape[1]
 
 
 def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: float | None = None,
@@ -322,35 +390,47 @@ def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: flo
     D ** -0.5.  With ``out`` and a large enough ``workspace`` the call only
     launches work on the stream.
     """
+    key = ("attend", _sig(q), _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(lens),
+           _sig(parents))
+    plan = _plans.get(key) or _remember(key, _plan_attend(q, k_pages, v_pages, page_table, lens,
+                                                          parents))
+    lay, N, R, Hq, q_row, q_head, max_pages, ws_bytes, default_scale = plan
     torch = _torch()
+    others = dict(k_pages=k_pages, v_pages=v_pages, page_table=page_table, lens=lens,
+                  parents=parents, workspace=workspace)
+    if out is not None:
+        _check_out("o", out.o, q.dtype, q.shape)
+        _check_out("lse", out.lse, torch.float32, q.shape[:3], optional=True)
+        _check_out("status", out.status, torch.int32, (1,))
+        others.update(o=out.o, lse=out.lse, status=out.status)
+    _check_workspace(workspace)
+    dev = _on_device(q, others)
+    raw = _raw_stream(stream, dev)
+    device = q.device
+    if out is None:
+        out = AttendResult(torch.empty(q.shape, dtype=q.dtype, device=device),
+                           torch.empty(q.shape[:3], dtype=torch.float32, device=device)
+                           if want_lse else None, _new_status(dev, raw))
+    if workspace is None or _nbytes(workspace) < ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
+    st = psi_attend_block(lay, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                          max_pages, lens.data_ptr(), N, R, Hq, q.data_ptr(), q_row, q_head,
+                          _ptr(parents), default_scale if scale is None else scale,
+                          out.o.data_ptr(), _ptr(out.lse), out.status.data_ptr(),
+                          workspace.data_ptr(), _nbytes(workspace), raw)
+    _check(st, "psi_attend_block")
+    return out
+
+
+def _plan_attend(q, k_pages, v_pages, page_table, lens, parents):
     N, R = _block(q, page_table, lens, parents)
     lay = _layout(k_pages, v_pages, layered=False)
     Hq, D = q.shape[2], lay.head_dim
     q_row, q_head = _heads("q", q, N, R, Hq, D, k_pages.dtype)
-    if out is not None:
-        _check_out("o", out.o, q.dtype, (N, R, Hq, D))
-        _check_out("lse", out.lse, torch.float32, (N, R, Hq), optional=True)
-        _check_out("status", out.status, torch.int32, (1,))
-    _check_workspace(workspace)
-    dev = _device_of(q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, lens=lens,
-                     parents=parents, workspace=workspace,
-                     **({} if out is None else dict(o=out.o, lse=out.lse, status=out.status)))
-    if out is None:
-        out = AttendResult(torch.empty(N, R, Hq, D, dtype=q.dtype, device=dev),
-                           torch.empty(N, R, Hq, dtype=torch.float32, device=dev)
-                           if want_lse else None, _new_status(dev))
-    ws_bytes = psi_attend_block_workspace_bytes(lay, N, R, Hq, page_table.shape[1])
-    if ws_bytes == 0:  # invalid sizes: let the ABI report the precise status
-        workspace = None
-    elif workspace is None or _nbytes(workspace) < ws_bytes:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    st = psi_attend_block(lay, _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-                          page_table.shape[1], _ptr(lens), N, R, Hq, _ptr(q), q_row, q_head,
-                          _ptr(parents), float(D ** -0.5 if scale is None else scale),
-                          _ptr(out.o), _ptr(out.lse), _ptr(out.status), _ptr(workspace),
-                          _nbytes(workspace), _stream(stream))
-    _check(st, "psi_attend_block")
-    return out
+    max_pages = page_table.shape[1]
+    # (0 for sizes that the call itself refuses)
+    return lay, N, R, Hq, q_row, q_head, max_pages, \
+        psi_attend_block_workspace_bytes(lay, N, R, Hq, max_pages), D ** -0.5
 
 
 def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, stream=None,
@@ -361,7 +441,30 @@ def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, strea
     int32 [N] as :func:`verify_tree_greedy` and :func:`verify_tree_sampled`
     return them.  Returns the new lengths (``out.lens`` is not ``lens``).
     """
+    key = ("commit", _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(lens), _sig(path_nodes),
+           _sig(path_len))
+    plan = _plans.get(key) or _remember(key, _plan_commit(k_pages, v_pages, page_table, lens,
+                                                          path_nodes, path_len))
+    lay, N, M, max_pages = plan
     torch = _torch()
+    others = dict(v_pages=v_pages, page_table=page_table, lens=lens, path_nodes=path_nodes,
+                  path_len=path_len)
+    if out is not None:
+        _check_out("lens", out.lens, torch.int32, (N,))
+        _check_out("status", out.status, torch.int32, (1,))
+        others.update(out_lens=out.lens, status=out.status)
+    dev = _on_device(k_pages, others)
+    raw = _raw_stream(stream, dev)
+    if out is None:
+        out = CommitResult(torch.empty_like(lens), _new_status(dev, raw))
+    st = psi_cache_commit(lay, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                          max_pages, lens.data_ptr(), N, M, path_nodes.data_ptr(),
+                          path_len.data_ptr(), out.lens.data_ptr(), out.status.data_ptr(), raw)
+    _check(st, "psi_cache_commit")
+    return out
+
+
+def _plan_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len):
     lay = _layout(k_pages, v_pages, layered=True)
     if page_table.dim() != 2 or path_nodes.dim() != 2:
         raise ValueError("page_table must be [N, max_pages], path_nodes [N, M]")
@@ -370,36 +473,37 @@ def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, strea
     _int32("lens", lens, (N,))
     _int32("path_nodes", path_nodes, (N, M))
     _int32("path_len", path_len, (N,))
-    if out is not None:
-        _check_out("lens", out.lens, torch.int32, (N,))
-        _check_out("status", out.status, torch.int32, (1,))
-    dev = _device_of(k_pages, v_pages=v_pages, page_table=page_table, lens=lens,
-                     path_nodes=path_nodes, path_len=path_len,
-                     **({} if out is None else dict(out_lens=out.lens, status=out.status)))
-    if out is None:
-        out = CommitResult(torch.empty_like(lens), _new_status(dev))
-    st = psi_cache_commit(lay, _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-                          page_table.shape[1], _ptr(lens), N, M, _ptr(path_nodes),
-                          _ptr(path_len), _ptr(out.lens), _ptr(out.status), _stream(stream))
-    _check(st, "psi_cache_commit")
-    return out
+    return lay, N, M, page_table.shape[1]
 
 
-def _state(name, s: PageState, N, max_pages, P):
-    for field, shape in (("table", (N, max_pages)), ("counts", (N,)), ("refs", (P,)),
-                         ("free", (P,)), ("n_free", (1,))):
+_STATE = ("table", "counts", "refs", "free", "n_free")
+
+
+def _check_state(name, s: PageState, N, max_pages, P):
+    for field, shape in zip(_STATE, ((N, max_pages), (N,), (P,), (P,), (1,))):
         _int32(f"{name}.{field}", getattr(s, field), shape)
-    return PageStatePtrs(_ptr(s.table), _ptr(s.counts), _ptr(s.refs), _ptr(s.free),
-                         _ptr(s.n_free))
 
 
-def _state_tensors(name, s: PageState):
-    return {f"{name}.{f}": getattr(s, f) for f in ("table", "counts", "refs", "free", "n_free")}
+def _state_ptrs(s: PageState):
+    return PageStatePtrs(s.table.data_ptr(), s.counts.data_ptr(), s.refs.data_ptr(),
+                         s.free.data_ptr(), s.n_free.data_ptr())
 
 
-def _like(s: PageState) -> PageState:
+def _state_sig(s: PageState):
+    return tuple(_sig(getattr(s, f)) for f in _STATE)
+
+
+def _named(name, s: PageState):
+    return {f"{name}.{f}": getattr(s, f) for f in _STATE}
+
+
+def _like(s: PageState, N, max_pages, P) -> PageState:
+    """A state of the same sizes, in one allocation."""
     torch = _torch()
-    return PageState(*(torch.empty_like(t) for t in (s.table, s.counts, s.refs, s.free, s.n_free)))
+    table, refs, free, counts, n_free = torch.empty(
+        N * max_pages + 2 * P + N + 1, dtype=torch.int32, device=s.table.device).split(
+            (N * max_pages, P, P, N, 1))
+    return PageState(table.view(N, max_pages), counts, refs, free, n_free)
 
 
 def cache_resize(pages: PageState, lens, extra: int, page_size: int, stream=None,
@@ -407,26 +511,31 @@ def cache_resize(pages: PageState, lens, extra: int, page_size: int, stream=None
     """Fit each sequence's pages to lens[n] + extra positions
     (``psi_cache_resize``).  Returns a new state; with ``out.pages = pages``
     the state is changed in place."""
-    torch = _torch()
+    key = ("resize", _state_sig(pages), _sig(lens))
+    N, max_pages, P = _plans.get(key) or _remember(key, _plan_resize(pages, lens))
+    others = dict(lens=lens, **_named("pages", pages))
+    if out is not None:
+        _check_state("out.pages", out.pages, N, max_pages, P)
+        _check_out("status", out.status, _torch().int32, (1,))
+        others.update(_named("out.pages", out.pages), status=out.status)
+    dev = _on_device(pages.table, others)
+    raw = _raw_stream(stream, dev)
+    if out is None:
+        out = ResizeResult(_like(pages, N, max_pages, P), _new_status(dev, raw))
+    st = psi_cache_resize(N, max_pages, P, page_size, lens.data_ptr(), extra, _state_ptrs(pages),
+                          _state_ptrs(out.pages), out.status.data_ptr(), raw)
+    _check(st, "psi_cache_resize")
+    return out
+
+
+def _plan_resize(pages, lens):
     if pages.table.dim() != 2:
         raise ValueError("pages.table must be [N, max_pages]")
     N, max_pages = pages.table.shape
     P = pages.refs.numel()
-    src = _state("pages", pages, N, max_pages, P)
+    _check_state("pages", pages, N, max_pages, P)
     _int32("lens", lens, (N,))
-    if out is not None:
-        _state("out.pages", out.pages, N, max_pages, P)
-        _check_out("status", out.status, torch.int32, (1,))
-    dev = _device_of(pages.table, lens=lens, **_state_tensors("pages", pages),
-                     **({} if out is None else dict(_state_tensors("out.pages", out.pages),
-                                                    status=out.status)))
-    if out is None:
-        out = ResizeResult(_like(pages), _new_status(dev))
-    st = psi_cache_resize(N, max_pages, P, page_size, _ptr(lens), extra, src,
-                          _state("out.pages", out.pages, N, max_pages, P), _ptr(out.status),
-                          _stream(stream))
-    _check(st, "psi_cache_resize")
-    return out
+    return N, max_pages, P
 
 
 def cache_fork(k_pages, v_pages, pages: PageState, lens, src, dst, workspace=None, stream=None,
@@ -437,33 +546,42 @@ def cache_fork(k_pages, v_pages, pages: PageState, lens, src, dst, workspace=Non
     k_pages, v_pages [L, P, S, H, D]; src, dst int32 [K].  Returns a new
     state and lengths; ``out`` may name the given ones (in place).
     """
+    key = ("fork", _sig(k_pages), _sig(v_pages), _state_sig(pages), _sig(lens), _sig(src),
+           _sig(dst))
+    plan = _plans.get(key) or _remember(key, _plan_fork(k_pages, v_pages, pages, lens, src, dst))
+    lay, N, max_pages, P, K, ws_bytes = plan
     torch = _torch()
+    others = dict(v_pages=v_pages, lens=lens, src=src, dst=dst, workspace=workspace,
+                  **_named("pages", pages))
+    if out is not None:
+        _check_state("out.pages", out.pages, N, max_pages, P)
+        _check_out("lens", out.lens, torch.int32, (N,))
+        _check_out("status", out.status, torch.int32, (1,))
+        others.update(_named("out.pages", out.pages), out_lens=out.lens, status=out.status)
+    _check_workspace(workspace)
+    dev = _on_device(k_pages, others)
+    raw = _raw_stream(stream, dev)
+    if out is None:
+        out = ForkResult(_like(pages, N, max_pages, P), torch.empty_like(lens),
+                         _new_status(dev, raw))
+    if workspace is None or _nbytes(workspace) < ws_bytes:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=k_pages.device)
+    st = psi_cache_fork(lay, k_pages.data_ptr(), v_pages.data_ptr(), N, max_pages,
+                        lens.data_ptr(), out.lens.data_ptr(), _state_ptrs(pages),
+                        _state_ptrs(out.pages), K, src.data_ptr(), dst.data_ptr(),
+                        out.status.data_ptr(), workspace.data_ptr(), _nbytes(workspace), raw)
+    _check(st, "psi_cache_fork")
+    return out
+
+
+def _plan_fork(k_pages, v_pages, pages, lens, src, dst):
     lay = _layout(k_pages, v_pages, layered=True)
     if pages.table.dim() != 2 or src.dim() != 1:
         raise ValueError("pages.table must be [N, max_pages], src and dst [K]")
     N, max_pages = pages.table.shape
     P, K = lay.num_pages, src.shape[0]
-    state = _state("pages", pages, N, max_pages, P)
+    _check_state("pages", pages, N, max_pages, P)
     _int32("lens", lens, (N,))
     _int32("src", src, (K,))
     _int32("dst", dst, (K,))
-    if out is not None:
-        _state("out.pages", out.pages, N, max_pages, P)
-        _check_out("lens", out.lens, torch.int32, (N,))
-        _check_out("status", out.status, torch.int32, (1,))
-    _check_workspace(workspace)
-    dev = _device_of(k_pages, v_pages=v_pages, lens=lens, src=src, dst=dst, workspace=workspace,
-                     **_state_tensors("pages", pages),
-                     **({} if out is None else dict(_state_tensors("out.pages", out.pages),
-                                                    out_lens=out.lens, status=out.status)))
-    if out is None:
-        out = ForkResult(_like(pages), torch.empty_like(lens), _new_status(dev))
-    ws_bytes = psi_cache_fork_workspace_bytes(K)
-    if ws_bytes and (workspace is None or _nbytes(workspace) < ws_bytes):
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
-    st = psi_cache_fork(lay, _ptr(k_pages), _ptr(v_pages), N, max_pages, _ptr(lens),
-                        _ptr(out.lens), state, _state("out.pages", out.pages, N, max_pages, P), K,
-                        _ptr(src), _ptr(dst), _ptr(out.status), _ptr(workspace),
-                        _nbytes(workspace), _stream(stream))
-    _check(st, "psi_cache_fork")
-    return out
+    return lay, N, max_pages, P, K, psi_cache_fork_workspace_bytes(K)
