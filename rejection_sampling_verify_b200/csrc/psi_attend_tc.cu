@@ -17,10 +17,18 @@
 // rounded to bf16 (half a step of 2^-8) for the product, as its operand must
 // be; the sums take them unrounded.
 //
-// Warps: 0-3 softmax, 4-6 load keys and values, 7 issues the products.
+// Loads: where pages are multiples of 8 slots, a tile is a few boxes of a
+// tensor map over the pool (TMA writes the swizzled operand directly, one
+// lane per box); other page sizes gather the rows' 16-byte chunks with
+// asynchronous copies.
+//
+// Warps: 0-3 softmax, then the loaders (one warp with TMA, four without),
+// and the last issues the products.
+#include <cuda.h>
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "psi_cache.h"
 #include "psi_tcgen05.cuh"
@@ -28,18 +36,18 @@
 namespace psi {
 namespace {
 
-constexpr int kTok = 128;  // positions per tile
-constexpr int kTcThreads = 256;
+constexpr int kTok = 128;   // positions per tile
 constexpr int kSoft = 128;  // softmax threads
-constexpr int kLoaders = 3;
-constexpr float kUnset = -1e30f;    // no reference yet
-constexpr float kHeadroom = 60.f;   // log2 units a score may exceed its reference by
+constexpr float kUnset = -1e30f;   // no reference yet
+constexpr float kHeadroom = 60.f;  // log2 units a score may exceed its reference by
 constexpr float kMinusInf = -INFINITY;
-constexpr float kLog2e_inv = 0.69314718055994531f;
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kSmemPerCta = 113 * 1024;  // two CTAs per SM
 
-template <int NT, int D>
+template <int NT, int D, bool kTma>
 struct TcShape {
+  static constexpr int kLoaders = kTma ? 1 : 4;  // warps
+  static constexpr int kThreads = kSoft + 32 * (kLoaders + 1);
   static constexpr int kTile = kTok * D * 2;  // bytes of keys or values per stage
   static constexpr int kQ = NT * D * 2;
   static constexpr int kP = NT * kTok * 2;
@@ -61,19 +69,64 @@ struct TcBarriers {
 
 __device__ __forceinline__ bool not_finite(uint16_t b) { return (b & 0x7F80u) == 0x7F80u; }
 
-template <int NT, int D>
-__global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, int32_t row_tiles) {
-  using T = TcShape<NT, D>;
+// x[0..15] = scores of packed rows c.. of this thread's position above their
+// references, in log2 units (-inf where a row does not see it); returns the
+// largest of them and `top`.
+template <bool kMasked>
+__device__ __forceinline__ float above(const float s[16], float scale2, const float *nrefs,
+                                       uint32_t seen, float top, float x[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 4) {
+    const float4 r = *reinterpret_cast<const float4 *>(nrefs + j);
+    const float2 k = make_float2(scale2, scale2);
+    const float2 a = fma2(make_float2(s[j], s[j + 1]), k, make_float2(r.x, r.y));
+    const float2 b = fma2(make_float2(s[j + 2], s[j + 3]), k, make_float2(r.z, r.w));
+    x[j] = a.x;
+    x[j + 1] = a.y;
+    x[j + 2] = b.x;
+    x[j + 3] = b.y;
+  }
+  if (kMasked) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = (seen >> j) & 1u ? x[j] : kMinusInf;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
+  return top;
+}
+
+// 2^x of 16 rows to the sums and, as bf16, to the operand P^T.
+__device__ __forceinline__ void weights(float x[16], float *l, uint8_t *pt) {
+  uint32_t w[8];
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    const float2 p = make_float2(fast_exp2(x[j]), fast_exp2(x[j + 1]));
+    const float2 t = add2(make_float2(l[j], l[j + 1]), p);
+    l[j] = t.x;
+    l[j + 1] = t.y;
+    const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+    w[j / 2] = *reinterpret_cast<const uint32_t *>(&b);
+  }
+  *reinterpret_cast<uint4 *>(pt) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint4 *>(pt + 2048) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+template <int NT, int D, bool kTma>
+__global__ void __launch_bounds__(TcShape<NT, D, kTma>::kThreads, 2)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, AttendArgs a, int32_t row_tiles) {
+  using T = TcShape<NT, D, kTma>;
+  constexpr int kMmaWarp = 4 + T::kLoaders;
   extern __shared__ uint8_t raw[];
   uint8_t *base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   uint8_t *ring = base;
   uint8_t *qs = ring + T::kStages * T::kTile;
   uint8_t *ps = qs + T::kQ;
   uint32_t *desc = reinterpret_cast<uint32_t *>(ps + T::kPBufs * T::kP);  // [R][kMaskWords]
-  float *refs = reinterpret_cast<float *>(desc + PSI_MAX_BLOCK_ROWS * T::kMaskWords);  // [NT]
-  float *facs = refs + NT;                                                             // [NT]
-  float *sums = facs + NT;                                                             // [NT]
-  float *wred = sums + NT;                                                             // [4][NT]
+  float *nrefs = reinterpret_cast<float *>(desc + PSI_MAX_BLOCK_ROWS * T::kMaskWords);  // [NT]
+  float *facs = nrefs + NT;                                                             // [NT]
+  float *sums = facs + NT;                                                              // [NT]
+  float *wred = sums + NT;                                                              // [4][NT]
   TcBarriers *bars = reinterpret_cast<TcBarriers *>(wred + 4 * NT);
   static_assert(sizeof(TcBarriers) <= 512, "");
 
@@ -99,7 +152,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
   const int end = begin + per < total ? begin + per : total;
   const int tiles = (end - begin + kTok - 1) / kTok;
   if (tiles == 0) {  // (only where the length is split) nothing in this range
-    for (int j = tid; j < NT && row0 + j < rows; j += kTcThreads) {
+    for (int j = tid; j < NT && row0 + j < rows; j += T::kThreads) {
       const int pr = row0 + j;
       const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
       a.part_ml[row * a.splits + split] = make_float2(kMinusInf, 0.f);
@@ -109,7 +162,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
 
   if (tid == 0) {
     for (int s = 0; s < T::kStages; ++s) {
-      mbar_init(&bars->full[s], 32);
+      mbar_init(&bars->full[s], kTma ? 1 : 32 * T::kLoaders);
       mbar_init(&bars->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -124,46 +177,68 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
     for (int w = 0; w < kBlockWords; ++w) bars->fix_tokens[w] = 0;
     fence_mbar_init();
   }
-  if (warp == 7) tmem_alloc(&bars->tmem, T::kCols);
+  if (warp == kMmaWarp) tmem_alloc(&bars->tmem, T::kCols);
   __syncthreads();
   const uint32_t tmem = bars->tmem;
   volatile uint32_t *gave_up = &bars->gave_up;
 
-  if (warp >= 4 && warp < 4 + kLoaders) {
-    // ---- loaders: items 2i (keys of tile i) and 2i + 1 (its values), one
-    // warp each.  A lane looks four positions' pages up; a row's 16-byte
-    // chunks are swizzled by the row, as the products' operands expect.
-    constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
-    const int chunk = lane % kLanesPerRow;
-    for (int item = 0; item < 2 * tiles; ++item) {
-      // a stage is one warp's: it meets the stage's phases in order
-      const int slot = item % T::kStages, t0 = begin + item / 2 * kTok;
-      if (slot % kLoaders != warp - 4) continue;
-      int64_t offs[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = t0 + 32 * i + lane;
-        offs[i] = t < end ? slot_offset(a.g, table, t) : -1;
+  if (warp >= 4 && warp < kMmaWarp) {
+    // ---- loaders: item 2i is the keys of tile i, item 2i + 1 its values
+    if constexpr (kTma) {
+      // One lane per box of `a.box` positions and 64 elements.  Boxes lie
+      // inside a page: tiles start at multiples of 128 positions, and a box
+      // divides the page size.
+      const int boxes = kTok / a.box, mine = lane % boxes, sub = lane / boxes;
+      const int in_tile = mine * a.box;
+      for (int i = 0; i < tiles; ++i) {
+        const int t = begin + i * kTok + in_tile;
+        const int page = sub < D / 64 && t < end ? page_of(a.g, table, t) : -1;
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * a.box * 128;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int item = 2 * i + kv, slot = item % T::kStages;
+          bool ok = true;
+          if (item >= T::kStages)
+            ok = wait_or_give_up(&bars->empty[slot], (item / T::kStages - 1) & 1, gave_up);
+          if (!__all_sync(0xFFFFFFFFu, ok)) {
+            i = tiles;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&bars->full[slot], bytes);
+          __syncwarp();
+          if (page >= 0)
+            tensor_load(smem_addr(ring + slot * T::kTile) + sub * (kTok * 128) + in_tile * 128,
+                        kv ? &vmap : &kmap, sub * 64, t % a.g.page_size, page, h,
+                        &bars->full[slot]);
+        }
       }
-      if (item >= T::kStages &&
-          !wait_or_give_up(&bars->empty[slot], (item / T::kStages - 1) & 1, gave_up))
-        break;
-      const uint16_t *pool = static_cast<const uint16_t *>(item & 1 ? a.v : a.k) +
-                             (int64_t)h * a.g.head_stride + chunk * 8;
-      const uint32_t dst = smem_addr(ring + slot * T::kTile) + chunk / 8 * (kTok * 128);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
+    } else {
+      // A warp takes 32 positions of every tile: a lane looks one position's
+      // page up, and a row's 16-byte chunks are swizzled by the row, as the
+      // products' operands expect.
+      constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
+      const int chunk = lane % kLanesPerRow, part = (warp - 4) * 32;
+      for (int item = 0; item < 2 * tiles; ++item) {
+        const int slot = item % T::kStages, t = begin + item / 2 * kTok + part + lane;
+        const int64_t mine = t < end ? slot_offset(a.g, table, t) : -1;
+        bool ok = true;
+        if (item >= T::kStages)
+          ok = wait_or_give_up(&bars->empty[slot], (item / T::kStages - 1) & 1, gave_up);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        const uint16_t *pool = static_cast<const uint16_t *>(item & 1 ? a.v : a.k) +
+                               (int64_t)h * a.g.head_stride + chunk * 8;
+        const uint32_t dst = smem_addr(ring + slot * T::kTile) + chunk / 8 * (kTok * 128);
 #pragma unroll 4
         for (int s = 0; s < 32; s += kRowsPerStep) {
-          const int from = s + lane / kLanesPerRow, row = 32 * i + from;
-          const int64_t off = __shfl_sync(0xFFFFFFFFu, offs[i], from);
+          const int from = s + lane / kLanesPerRow, row = part + from;
+          const int64_t off = __shfl_sync(0xFFFFFFFFu, mine, from);
           copy16(dst + row * 128 + ((chunk % 8) ^ (row % 8)) * 16, pool + (off < 0 ? 0 : off),
                  off >= 0);
         }
-      copy_arrive(&bars->full[slot]);
+        copy_arrive(&bars->full[slot]);
+      }
+      copy_wait_all();
     }
-    copy_wait_all();
-  } else if (warp == 7) {
+  } else if (warp == kMmaWarp) {
     // ---- products, issued by one lane
     if (lane == 0) {
       constexpr uint32_t kScores = product_shape(NT, false, false);
@@ -230,7 +305,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
     mbar_arrive(&bars->q_full);
     // which rows see which of the block's positions; which rows belong to it
     for (int i = tid; i < a.R * T::kMaskWords; i += kSoft) desc[i] = 0;
-    for (int j = tid; j < NT; j += kSoft) refs[j] = kUnset;
+    for (int j = tid; j < NT; j += kSoft) nrefs[j] = -kUnset;
     bool bad_page = false;
     for (int i = begin / a.g.page_size + tid; i <= (end - 1) / a.g.page_size; i += kSoft)
       bad_page |= table[i] < 0 || table[i] >= a.g.num_pages;
@@ -256,40 +331,49 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
     float l[NT];  // sums of this thread's positions
 #pragma unroll
     for (int j = 0; j < NT; ++j) l[j] = 0.f;
-    bool ok = true;
+    // with few rows a tile's scores stay in registers between the two steps
+    constexpr bool kKeep = NT <= 48;
+    float kept[kKeep ? NT : 1];
     for (int i = 0; i < tiles; ++i) {
       const int t = begin + i * kTok + tid;
       // rows that see this thread's position
       uint32_t seen[T::kMaskWords];
-      const bool all = begin + (i + 1) * kTok <= (len < end ? len : end) && !bad_page;
-#pragma unroll
-      for (int w = 0; w < T::kMaskWords; ++w) seen[w] = 0xFFFFFFFFu;
-      if (!all) {
-        const bool there = t < end && page_of(a.g, table, t) >= 0;
+      const bool masked = begin + (i + 1) * kTok > (len < end ? len : end) || bad_page;
+      bool there = true;
+      if (masked) {
+        there = t < end && page_of(a.g, table, t) >= 0;
 #pragma unroll
         for (int w = 0; w < T::kMaskWords; ++w)
           seen[w] = !there ? 0u : t < len ? 0xFFFFFFFFu : desc[(t - len) * T::kMaskWords + w];
       }
-      ok = wait_or_give_up(&bars->s_full[i & 1], (i >> 1) & 1, gave_up);
-      if (named_or(1, kSoft, !ok)) {
-        ok = false;
-        break;
-      }
+      // (a wait that gives up leaves garbage behind and the status says so)
+      wait_or_give_up(&bars->s_full[i & 1], (i >> 1) & 1, gave_up);
+      __syncwarp();
       tc_fence_after();
       const uint32_t st = tmem + lanes + (i & 1) * NT;
-      float top = kMinusInf;  // how far a score exceeds its reference
+      // how far scores exceed their references
+      const auto exceed = [&](auto mask) {
+        float top = kMinusInf;
+        if constexpr (kKeep) {
 #pragma unroll
-      for (int c = 0; c < NT; c += 16) {
-        float s[16];
-        tmem_ld16(st + c, s);
-        tmem_wait_ld();
+          for (int c = 0; c < NT; c += 16) tmem_ld16(st + c, kept + c);
+          tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float x = fmaf(s[j], a.scale2, -refs[c + j]);
-          const bool sees = (seen[(c + j) / 32] >> ((c + j) % 32)) & 1u;
-          top = fmaxf(top, sees ? x : kMinusInf);
+          for (int c = 0; c < NT; c += 16)
+            top = above<mask.value>(kept + c, a.scale2, nrefs + c, seen[c / 32] >> (c % 32), top,
+                                    kept + c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < NT; c += 16) {
+            float s[16];
+            tmem_ld16(st + c, s);
+            tmem_wait_ld();
+            top = above<mask.value>(s, a.scale2, nrefs + c, seen[c / 32] >> (c % 32), top, s);
+          }
         }
-      }
+        return top;
+      };
+      const float top = masked ? exceed(std::true_type{}) : exceed(std::false_type{});
       if (named_or(1, kSoft, top > kHeadroom)) {
         // raise those references to the tile's maxima and rescale what is there
 #pragma unroll
@@ -299,8 +383,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const bool sees = (seen[(c + j) / 32] >> ((c + j) % 32)) & 1u;
-            const float m = warp_max(sees ? s[j] * a.scale2 : kMinusInf);
+            const bool sees = !masked || ((seen[(c + j) / 32] >> ((c + j) % 32)) & 1u);
+            const float m = warp_max_f32(sees ? s[j] * a.scale2 : kMinusInf);
             if (lane == 0) wred[warp * NT + c + j] = m;
           }
         }
@@ -309,67 +393,67 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
           const float m = fmaxf(fmaxf(wred[tid], wred[NT + tid]),
                                 fmaxf(wred[2 * NT + tid], wred[3 * NT + tid]));
           // (each row by its own scores: what other rows see does not touch its bits)
-          const float old = refs[tid], now = m > old + kHeadroom ? m : old;
+          const float old = -nrefs[tid], now = m > old + kHeadroom ? m : old;
           facs[tid] = fast_exp2(old - now);
-          refs[tid] = now;
+          nrefs[tid] = -now;
         }
-        if (i > 0) ok = wait_or_give_up(&bars->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
-        if (named_or(1, kSoft, !ok)) {
-          ok = false;
-          break;
-        }
+        if (i > 0) wait_or_give_up(&bars->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
+        named_sync(1, kSoft);
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < NT; c += 16) {
-          float o[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) l[c + j] *= facs[c + j];
           if (i > 0) {
+            float o[16];
             tmem_ld16(tmem + lanes + 2 * NT + c, o);
             tmem_wait_ld();
-          }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float f = facs[c + j];
-            l[c + j] *= f;
-            o[j] *= f;
+            for (int j = 0; j < 16; ++j) o[j] *= facs[c + j];
+            tmem_st16(tmem + lanes + 2 * NT + c, o);
           }
-          if (i > 0) tmem_st16(tmem + lanes + 2 * NT + c, o);
         }
         tmem_wait_st();
+        if constexpr (kKeep) {
+          if (masked) exceed(std::true_type{});
+          else exceed(std::false_type{});
+        }
       }
       // the buffer of P^T is free once its last product is done
       if (i >= T::kPBufs) {
         const int x = i - T::kPBufs;
-        ok = wait_or_give_up(&bars->pv_done[x & 1], (x >> 1) & 1, gave_up);
+        wait_or_give_up(&bars->pv_done[x & 1], (x >> 1) & 1, gave_up);
+        __syncwarp();
       }
       uint8_t *pt = ps + i % T::kPBufs * T::kP + tid / 8 * 128 + tid % 8 * 16;
 #pragma unroll
       for (int c = 0; c < NT; c += 16) {
-        float s[16];
-        tmem_ld16(st + c, s);
-        tmem_wait_ld();
-        uint32_t packed[8];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const bool sees = (seen[(c + j) / 32] >> ((c + j) % 32)) & 1u;
-          const float x = fmaf(s[j], a.scale2, -refs[c + j]);
-          s[j] = fast_exp2(sees ? x : kMinusInf);
-          l[c + j] += s[j];
+        if constexpr (kKeep) {
+          weights(kept + c, l + c, pt + c / 8 * 2048);
+        } else {
+          float s[16];
+          tmem_ld16(st + c, s);
+          tmem_wait_ld();
+          if (masked)
+            above<true>(s, a.scale2, nrefs + c, seen[c / 32] >> (c % 32), 0.f, s);
+          else
+            above<false>(s, a.scale2, nrefs + c, 0u, 0.f, s);
+          weights(s, l + c, pt + c / 8 * 2048);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(s[2 * j], s[2 * j + 1]);
-          packed[j] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-        *reinterpret_cast<uint4 *>(pt + c / 8 * 2048) =
-            make_uint4(packed[0], packed[1], packed[2], packed[3]);
-        *reinterpret_cast<uint4 *>(pt + (c / 8 + 1) * 2048) =
-            make_uint4(packed[4], packed[5], packed[6], packed[7]);
       }
-      if (a.R > 1 && t >= len && t < end) {
+      if (masked && !there) {
+        // what lies here is no value of the sequence: 0 * NaN is not 0
+        const int item = 2 * i + 1, slot = item % T::kStages;
+        wait_or_give_up(&bars->full[slot], (item / T::kStages) & 1, gave_up);
+        uint8_t *v = ring + slot * T::kTile + tid * 128;
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4 *>(v + c / 8 * (kTok * 128) + c % 8 * 16) = make_uint4(0, 0, 0, 0);
+      }
+      if (a.R > 1 && there && t >= len) {
         // 0 * inf is not 0: a value of the block that some rows must not see
         // is taken out here if it is not finite, and added at the end
         const int item = 2 * i + 1, slot = item % T::kStages;
-        ok &= wait_or_give_up(&bars->full[slot], (item / T::kStages) & 1, gave_up);
+        wait_or_give_up(&bars->full[slot], (item / T::kStages) & 1, gave_up);
         uint8_t *v = ring + slot * T::kTile + tid * 128;
         bool fix = false;
         for (int c = 0; c < D / 8; ++c) {
@@ -393,8 +477,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
     }
 
     // ---- results
-    if (ok)
-      ok = wait_or_give_up(&bars->pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, gave_up);
+    wait_or_give_up(&bars->pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, gave_up);
+    __syncwarp();
     tc_fence_after();
 #pragma unroll
     for (int c = 0; c < NT; c += 16) {  // add up the lanes: lane x ends with row c + x % 16
@@ -422,9 +506,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
       if (pr < rows) {
         const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
         if (a.splits > 1)
-          a.part_ml[row * a.splits + split] = make_float2(s == 0.f ? kMinusInf : refs[tid], s);
+          a.part_ml[row * a.splits + split] = make_float2(s == 0.f ? kMinusInf : -nrefs[tid], s);
         else if (a.out_lse)
-          a.out_lse[row] = s == 0.f ? kMinusInf : refs[tid] * kLog2e_inv + logf(s);
+          a.out_lse[row] = s == 0.f ? kMinusInf : -nrefs[tid] * kLn2 + logf(s);
       }
     }
     named_sync(1, kSoft);
@@ -465,35 +549,68 @@ __global__ void __launch_bounds__(kTcThreads, 2) attend_tc_kernel(AttendArgs a, 
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 7) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_free(tmem, T::kCols);
   }
   if (tid == 0 && bars->gave_up && a.dev_status) atomicOr(a.dev_status, PSI_DEV_TIMEOUT);
 }
 
-template <int NT, int D>
-cudaError_t launch_shape(const AttendArgs &a, int32_t row_tiles, int64_t ctas, cudaStream_t stream) {
-  using T = TcShape<NT, D>;
-  static DeviceOnce once;
-  const cudaError_t e = once([] {
-    return cudaFuncSetAttribute(attend_tc_kernel<NT, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                T::kSmem);
-  });
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attend_tc_kernel<NT, D>, dim3((unsigned)ctas), dim3(kTcThreads), T::kSmem,
-                    stream, a, row_tiles);
+// The pools as 4-dimensional tensors: element, slot, page, head.
+typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
 }
 
-template <int D>
-cudaError_t launch_dim(const AttendArgs &a, int nt, int32_t row_tiles, int64_t ctas,
-                       cudaStream_t stream) {
-  switch (nt) {
-    case 16: return launch_shape<16, D>(a, row_tiles, ctas, stream);
-    case 32: return launch_shape<32, D>(a, row_tiles, ctas, stream);
-    case 48: return launch_shape<48, D>(a, row_tiles, ctas, stream);
-    case 64: return launch_shape<64, D>(a, row_tiles, ctas, stream);
-    default: return launch_shape<80, D>(a, row_tiles, ctas, stream);
+bool pool_map(CUtensorMap *map, const AttendArgs &a, const void *pool) {
+  const auto bytes = [](int64_t elements) { return (cuuint64_t)(elements ? elements : 8) * 2; };
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.g.page_size,
+                              (cuuint64_t)a.g.num_pages, (cuuint64_t)a.kv_heads};
+  const cuuint64_t strides[3] = {bytes(a.g.slot_stride), bytes(a.g.page_stride),
+                                 bytes(a.g.head_stride)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)a.box, 1, 1}, steps[4] = {1, 1, 1, 1};
+  return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims,
+                        strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, int D, bool kTma>
+cudaError_t launch_shape(const AttendArgs &a, int32_t row_tiles, int64_t ctas, cudaStream_t stream) {
+  using T = TcShape<NT, D, kTma>;
+  static DeviceOnce once;
+  const cudaError_t e = once([] {
+    return cudaFuncSetAttribute(attend_tc_kernel<NT, D, kTma>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  CUtensorMap kmap = {}, vmap = {};
+  if (kTma && (!pool_map(&kmap, a, a.k) || !pool_map(&vmap, a, a.v))) return cudaErrorInvalidValue;
+  return launch_pdl(attend_tc_kernel<NT, D, kTma>, dim3((unsigned)ctas), dim3(T::kThreads),
+                    T::kSmem, stream, kmap, vmap, a, row_tiles);
+}
+
+template <int D, bool kTma>
+cudaError_t launch_dim(const AttendArgs &a, const AttendPlan &p, cudaStream_t stream) {
+  switch (p.rows) {
+    case 16: return launch_shape<16, D, kTma>(a, p.row_tiles, p.ctas, stream);
+    case 32: return launch_shape<32, D, kTma>(a, p.row_tiles, p.ctas, stream);
+    case 48: return launch_shape<48, D, kTma>(a, p.row_tiles, p.ctas, stream);
+    case 64: return launch_shape<64, D, kTma>(a, p.row_tiles, p.ctas, stream);
+    default: return launch_shape<80, D, kTma>(a, p.row_tiles, p.ctas, stream);
   }
 }
 
@@ -509,9 +626,16 @@ int attend_tc_rows(int rows) {
   return ((rows + tiles - 1) / tiles + 15) / 16 * 16;
 }
 
-cudaError_t launch_attend_tc(const AttendArgs &a, const AttendPlan &plan, cudaStream_t stream) {
-  return a.D == 128 ? launch_dim<128>(a, plan.rows, plan.row_tiles, plan.ctas, stream)
-                    : launch_dim<64>(a, plan.rows, plan.row_tiles, plan.ctas, stream);
+cudaError_t launch_attend_tc(AttendArgs a, const AttendPlan &plan, cudaStream_t stream) {
+  a.box = 1;  // the largest power of two that divides the page size, up to a tile
+  while (a.box < kTok && a.g.page_size % (2 * a.box) == 0) a.box *= 2;
+  // a swizzled operand repeats every 8 rows
+  const int64_t most = int64_t(1) << 39;  // (tensor maps take strides below 2^40 bytes)
+  const bool tma = a.box >= 8 && encode_tiled() != nullptr && a.g.slot_stride < most &&
+                   a.g.page_stride < most && a.g.head_stride < most;
+  if (a.D == 128)
+    return tma ? launch_dim<128, true>(a, plan, stream) : launch_dim<128, false>(a, plan, stream);
+  return tma ? launch_dim<64, true>(a, plan, stream) : launch_dim<64, false>(a, plan, stream);
 }
 
 }  // namespace psi

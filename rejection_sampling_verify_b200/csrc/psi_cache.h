@@ -23,6 +23,7 @@ struct AttendArgs {
   int32_t splits;
   float *part_o;   // [N * R * q_heads][splits][D], relative to part_ml's maximum
   float2 *part_ml; // [N * R * q_heads][splits]: maximum (log2 units), sum
+  int32_t box;     // positions per TMA box
 };
 struct AttendPlan {
   bool tc;        // on the tensor cores
@@ -39,7 +40,7 @@ cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan,
 // The tensor-core form (psi_attend_tc.cu).
 bool attend_tc_fits(psi_dtype dtype, int32_t D);
 int attend_tc_rows(int rows);
-cudaError_t launch_attend_tc(const AttendArgs &a, const AttendPlan &plan, cudaStream_t stream);
+cudaError_t launch_attend_tc(AttendArgs a, const AttendPlan &plan, cudaStream_t stream);
 
 struct AppendArgs {
   Paging g;
