@@ -22,8 +22,9 @@
 // lane per box); other page sizes gather the rows' 16-byte chunks with
 // asynchronous copies.
 //
-// Warps: 0-3 softmax, then the loaders (one warp with TMA, four without),
-// and the last issues the products.
+// Warps: 0-3 softmax; 4 loads keys and issues the products K Q^T; 5 loads
+// values and issues V^T P^T.  Keys and values have stages of their own, so
+// that the next keys load while the weights of this tile are at work.
 #include <cuda.h>
 #include <math.h>
 
@@ -38,6 +39,7 @@ namespace {
 
 constexpr int kTok = 128;   // positions per tile
 constexpr int kSoft = 128;  // softmax threads
+constexpr int kTcThreads = kSoft + 64;
 constexpr float kUnset = -1e30f;   // no reference yet
 constexpr float kHeadroom = 60.f;  // log2 units a score may exceed its reference by
 constexpr float kMinusInf = -INFINITY;
@@ -46,23 +48,22 @@ constexpr int kSmemPerCta = 113 * 1024;  // two CTAs per SM
 
 template <int NT, int D, bool kTma>
 struct TcShape {
-  static constexpr int kLoaders = kTma ? 1 : 4;  // warps
-  static constexpr int kThreads = kSoft + 32 * (kLoaders + 1);
   static constexpr int kTile = kTok * D * 2;  // bytes of keys or values per stage
   static constexpr int kQ = NT * D * 2;
   static constexpr int kP = NT * kTok * 2;
   static constexpr int kPBufs = NT <= 48 ? 2 : 1;
   static constexpr int kMaskWords = (NT + 31) / 32;
-  static constexpr int kSmall = PSI_MAX_BLOCK_ROWS * kMaskWords * 4 + 7 * NT * 4 + 512;
+  static constexpr int kSmall = PSI_MAX_BLOCK_ROWS * kMaskWords * 4 + 9 * NT * 4 + 512;
   static constexpr int kRoom = (kSmemPerCta - 1024 - kSmall - kQ - kPBufs * kP) / kTile;
   static constexpr int kStages = kRoom < 6 ? kRoom : 6;
+  static constexpr int kKStages = (kStages + 1) / 2, kVStages = kStages / 2;
   static constexpr int kSmem = 1024 + kStages * kTile + kQ + kPBufs * kP + kSmall;
   static constexpr int kCols = 3 * NT <= 64 ? 64 : 3 * NT <= 128 ? 128 : 256;
   static_assert(kStages >= 2 && 3 * NT <= 256 && NT % 16 == 0, "");
 };
 
 struct TcBarriers {
-  uint64_t full[6], empty[6], s_full[2], p_full[2], pv_done[2], q_full, drained;
+  uint64_t k_full[3], v_full[3], s_full[2], p_full[2], pv_done[2], q_full, drained[2];
   uint32_t tmem, gave_up, fix;
   uint32_t fix_tokens[kBlockWords];  // the block's positions whose values are not finite
 };
@@ -112,194 +113,206 @@ __device__ __forceinline__ void weights(float x[16], float *l, uint8_t *pt) {
 }
 
 template <int NT, int D, bool kTma>
-__global__ void __launch_bounds__(TcShape<NT, D, kTma>::kThreads, 2)
+__global__ void __launch_bounds__(kTcThreads, 2)
     attend_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, AttendArgs a, int32_t row_tiles) {
   using T = TcShape<NT, D, kTma>;
-  constexpr int kMmaWarp = 4 + T::kLoaders;
   extern __shared__ uint8_t raw[];
   uint8_t *base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
-  uint8_t *ring = base;
-  uint8_t *qs = ring + T::kStages * T::kTile;
+  uint8_t *kring = base, *vring = base + T::kKStages * T::kTile;
+  uint8_t *qs = base + T::kStages * T::kTile;
   uint8_t *ps = qs + T::kQ;
   uint32_t *desc = reinterpret_cast<uint32_t *>(ps + T::kPBufs * T::kP);  // [R][kMaskWords]
   float *nrefs = reinterpret_cast<float *>(desc + PSI_MAX_BLOCK_ROWS * T::kMaskWords);  // [NT]
   float *facs = nrefs + NT;                                                             // [NT]
   float *sums = facs + NT;                                                              // [NT]
   float *wred = sums + NT;                                                              // [4][NT]
-  TcBarriers *bars = reinterpret_cast<TcBarriers *>(wred + 4 * NT);
+  int64_t *out_row = reinterpret_cast<int64_t *>(wred + 4 * NT);                        // [NT]
+  TcBarriers *bars = reinterpret_cast<TcBarriers *>(out_row + NT);
   static_assert(sizeof(TcBarriers) <= 512, "");
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  int64_t id = blockIdx.x;
-  const int split = (int)(id % a.splits);
-  id /= a.splits;
-  const int tile_of_rows = (int)(id % row_tiles);
-  id /= row_tiles;
-  const int h = (int)(id % a.kv_heads);
-  const int n = (int)(id / a.kv_heads);
-  pdl_wait();
-  const int len = a.g.lens[n];
-  if (len < 0) return;  // the sequence is not there
-  const int G = a.q_heads / a.kv_heads;
-  const int rows = a.R * G, row0 = tile_of_rows * NT;
-  const int32_t *parents = a.parents ? a.parents + (int64_t)n * (a.R - 1) : nullptr;
-  const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
-  const int64_t cap = table_capacity(a.g), want = (int64_t)len + a.R;
-  const int total = (int)(want < cap ? want : cap);
-  const int per = ((total + a.splits - 1) / a.splits + kTok - 1) / kTok * kTok;
-  const int begin = split * per < total ? split * per : total;
-  const int end = begin + per < total ? begin + per : total;
-  const int tiles = (end - begin + kTok - 1) / kTok;
-  if (tiles == 0) {  // (only where the length is split) nothing in this range
-    for (int j = tid; j < NT && row0 + j < rows; j += T::kThreads) {
-      const int pr = row0 + j;
-      const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
-      a.part_ml[row * a.splits + split] = make_float2(kMinusInf, 0.f);
-    }
-    return;
-  }
-
   if (tid == 0) {
-    for (int s = 0; s < T::kStages; ++s) {
-      mbar_init(&bars->full[s], kTma ? 1 : 32 * T::kLoaders);
-      mbar_init(&bars->empty[s], 1);
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&bars->k_full[s], kTma ? 1 : 32);
+      mbar_init(&bars->v_full[s], kTma ? 1 : 32);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->s_full[b], 1);
       mbar_init(&bars->p_full[b], kSoft);
       mbar_init(&bars->pv_done[b], 1);
+      mbar_init(&bars->drained[b], 1);
     }
     mbar_init(&bars->q_full, kSoft);
-    mbar_init(&bars->drained, 1);
     bars->gave_up = 0;
     bars->fix = 0;
     for (int w = 0; w < kBlockWords; ++w) bars->fix_tokens[w] = 0;
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) tmem_alloc(&bars->tmem, T::kCols);
+  if (warp == 4) tmem_alloc(&bars->tmem, T::kCols);
+  if (kTma && tid == 5 * 32) {
+    prefetch_map(&kmap);
+    prefetch_map(&vmap);
+  }
+  pdl_wait();
+
+  int id = blockIdx.x;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int row0 = id % row_tiles * NT;
+  id /= row_tiles;
+  const int h = id % a.kv_heads;
+  const int n = id / a.kv_heads;
+  const int len = a.g.lens[n];
+  const int G = a.q_heads / a.kv_heads;
+  const int rows = a.R * G;
+  const int32_t *parents = a.parents ? a.parents + (int64_t)n * (a.R - 1) : nullptr;
+  const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
+  const int64_t cap = table_capacity(a.g), want = (int64_t)len + a.R;
+  const int total = len < 0 ? 0 : (int)(want < cap ? want : cap);  // 0: the sequence is not there
+  const int per = ((total + a.splits - 1) / a.splits + kTok - 1) / kTok * kTok;
+  const int begin = split * per < total ? split * per : total;
+  const int end = begin + per < total ? begin + per : total;
+  const int tiles = (end - begin + kTok - 1) / kTok;
+  if (tid < NT) {  // where the packed rows go
+    const int pr = row0 + tid;
+    out_row[tid] = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
+  }
   __syncthreads();
   const uint32_t tmem = bars->tmem;
   volatile uint32_t *gave_up = &bars->gave_up;
+  if (tiles == 0 && len >= 0 && tid < NT && row0 + tid < rows)
+    a.part_ml[out_row[tid] * a.splits + split] = make_float2(kMinusInf, 0.f);  // (only when split)
 
-  if (warp >= 4 && warp < kMmaWarp) {
-    // ---- loaders: item 2i is the keys of tile i, item 2i + 1 its values
-    if constexpr (kTma) {
-      // One lane per box of `a.box` positions and 64 elements.  Boxes lie
-      // inside a page: tiles start at multiples of 128 positions, and a box
-      // divides the page size.
-      const int boxes = kTok / a.box, mine = lane % boxes, sub = lane / boxes;
-      const int in_tile = mine * a.box;
-      for (int i = 0; i < tiles; ++i) {
+  if (tiles > 0 && (warp == 4 || warp == 5)) {
+    // ---- loads and products of keys (warp 4) or values (warp 5)
+    const bool keys = warp == 4;
+    const int stages = keys ? T::kKStages : T::kVStages;
+    uint8_t *ring = keys ? kring : vring;
+    uint64_t *full = keys ? bars->k_full : bars->v_full;
+    // One box (TMA) or one position of each 32 (copies) is a lane's to find:
+    // looked up one tile ahead.
+    const int boxes = kTma ? kTok / a.box : 1, in_tile = lane % boxes * a.box, sub = lane / boxes;
+    int page = -1;
+    int64_t offs[4];
+    const auto look_up = [&](int i) {
+      if constexpr (kTma) {
         const int t = begin + i * kTok + in_tile;
-        const int page = sub < D / 64 && t < end ? page_of(a.g, table, t) : -1;
+        page = sub < D / 64 && t < end ? page_of(a.g, table, t) : -1;
+      } else {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int t = begin + i * kTok + 32 * x + lane;
+          offs[x] = t < end ? slot_offset(a.g, table, t) : -1;
+        }
+      }
+    };
+    int loaded = 0;
+    const auto load = [&]() {
+      const int slot = loaded % stages;
+      const uint32_t dst = smem_addr(ring + slot * T::kTile);
+      if constexpr (kTma) {
+        // boxes lie inside a page: tiles start at multiples of 128
+        // positions, and a box divides the page size
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * a.box * 128;
-        for (int kv = 0; kv < 2; ++kv) {
-          const int item = 2 * i + kv, slot = item % T::kStages;
-          bool ok = true;
-          if (item >= T::kStages)
-            ok = wait_or_give_up(&bars->empty[slot], (item / T::kStages - 1) & 1, gave_up);
-          if (!__all_sync(0xFFFFFFFFu, ok)) {
-            i = tiles;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(&bars->full[slot], bytes);
-          __syncwarp();
-          if (page >= 0)
-            tensor_load(smem_addr(ring + slot * T::kTile) + sub * (kTok * 128) + in_tile * 128,
-                        kv ? &vmap : &kmap, sub * 64, t % a.g.page_size, page, h,
-                        &bars->full[slot]);
-        }
-      }
-    } else {
-      // A warp takes 32 positions of every tile: a lane looks one position's
-      // page up, and a row's 16-byte chunks are swizzled by the row, as the
-      // products' operands expect.
-      constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
-      const int chunk = lane % kLanesPerRow, part = (warp - 4) * 32;
-      for (int item = 0; item < 2 * tiles; ++item) {
-        const int slot = item % T::kStages, t = begin + item / 2 * kTok + part + lane;
-        const int64_t mine = t < end ? slot_offset(a.g, table, t) : -1;
-        bool ok = true;
-        if (item >= T::kStages)
-          ok = wait_or_give_up(&bars->empty[slot], (item / T::kStages - 1) & 1, gave_up);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        const uint16_t *pool = static_cast<const uint16_t *>(item & 1 ? a.v : a.k) +
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+        __syncwarp();
+        if (page >= 0)
+          tensor_load(dst + sub * (kTok * 128) + in_tile * 128, keys ? &kmap : &vmap, sub * 64,
+                      (begin + loaded * kTok + in_tile) % a.g.page_size, page, h, &full[slot]);
+      } else {
+        // rows' 16-byte chunks, swizzled by the row as the operands expect
+        constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
+        const int chunk = lane % kLanesPerRow;
+        const uint16_t *pool = static_cast<const uint16_t *>(keys ? a.k : a.v) +
                                (int64_t)h * a.g.head_stride + chunk * 8;
-        const uint32_t dst = smem_addr(ring + slot * T::kTile) + chunk / 8 * (kTok * 128);
+        const uint32_t to = dst + chunk / 8 * (kTok * 128);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
 #pragma unroll 4
-        for (int s = 0; s < 32; s += kRowsPerStep) {
-          const int from = s + lane / kLanesPerRow, row = part + from;
-          const int64_t off = __shfl_sync(0xFFFFFFFFu, mine, from);
-          copy16(dst + row * 128 + ((chunk % 8) ^ (row % 8)) * 16, pool + (off < 0 ? 0 : off),
-                 off >= 0);
-        }
-        copy_arrive(&bars->full[slot]);
+          for (int s = 0; s < 32; s += kRowsPerStep) {
+            const int from = s + lane / kLanesPerRow, row = 32 * x + from;
+            const int64_t off = __shfl_sync(0xFFFFFFFFu, offs[x], from);
+            copy16(to + row * 128 + ((chunk % 8) ^ (row % 8)) * 16, pool + (off < 0 ? 0 : off),
+                   off >= 0);
+          }
+        copy_arrive(&full[slot]);
       }
-      copy_wait_all();
-    }
-  } else if (warp == kMmaWarp) {
-    // ---- products, issued by one lane
-    if (lane == 0) {
-      constexpr uint32_t kScores = product_shape(NT, false, false);
-      constexpr uint32_t kValues = product_shape(NT, true, true);
-      const uint32_t q = smem_addr(qs), p = smem_addr(ps), kv = smem_addr(ring);
-      const auto scores = [&](int i) {
-        const int item = 2 * i, slot = item % T::kStages;
-        if (!wait_or_give_up(&bars->full[slot], (item / T::kStages) & 1, gave_up)) return false;
-        fence_async_shared();
-        tc_fence_after();
+      if (++loaded < tiles) look_up(loaded);
+    };
+    look_up(0);
+    while (loaded < stages && loaded < tiles) load();
+
+    constexpr uint32_t kScores = product_shape(NT, false, false);
+    constexpr uint32_t kValues = product_shape(NT, true, true);
+    bool ok = !keys || wait_or_give_up(&bars->q_full, 0, gave_up);
+    for (int i = 0; i < tiles; ++i) {
+      const int slot = i % stages, b = i & 1, phase = (i >> 1) & 1;
+      const uint32_t at = smem_addr(ring + slot * T::kTile);
+      ok = ok && wait_or_give_up(&full[slot], (i / stages) & 1, gave_up);
+      if (keys) {
+        // S^T's buffer is free once the tile before last has its weights
+        if (i >= 2) ok = ok && wait_or_give_up(&bars->p_full[b], ((i - 2) >> 1) & 1, gave_up);
+      } else {
+        ok = ok && wait_or_give_up(&bars->p_full[b], phase, gave_up);
+      }
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      fence_async_shared();
+      tc_fence_after();
+      if (lane == 0) {
+        if (keys) {
+          const uint32_t q = smem_addr(qs);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t at = kv + slot * T::kTile + k / 4 * (kTok * 128) + k % 4 * 32;
-          const uint32_t qt = q + k / 4 * (NT * 128) + k % 4 * 32;
-          tc_product(tmem + (i & 1) * NT, operand(at, 16, 1024, 2), operand(qt, 16, 1024, 2),
-                     kScores, k > 0);
-        }
-        tc_commit(&bars->empty[slot]);
-        tc_commit(&bars->s_full[i & 1]);
-        return true;
-      };
-      bool ok = wait_or_give_up(&bars->q_full, 0, gave_up) && scores(0);
-      if (ok && tiles > 1) ok = scores(1);
-      for (int i = 0; ok && i < tiles; ++i) {
-        const int item = 2 * i + 1, slot = item % T::kStages;
-        ok = wait_or_give_up(&bars->p_full[i & 1], (i >> 1) & 1, gave_up) &&
-             wait_or_give_up(&bars->full[slot], (item / T::kStages) & 1, gave_up);
-        if (!ok) break;
-        fence_async_shared();
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < kTok / 16; ++k) {
+          for (int k = 0; k < D / 16; ++k)
+            tc_product(tmem + b * NT,
+                       operand(at + k / 4 * (kTok * 128) + k % 4 * 32, 16, 1024, 2),
+                       operand(q + k / 4 * (NT * 128) + k % 4 * 32, 16, 1024, 2), kScores, k > 0);
+          tc_commit(&bars->s_full[b]);
+        } else {
           // V^T: 64-element columns a sub-tile apart (the same one twice for
           // D = 64: the upper half of O^T is not read), 8 positions 1 KB
           // apart.  P^T: 8 positions 128 bytes apart, 8 rows 2 KB.
-          const uint32_t at = kv + slot * T::kTile + k * 2048;
-          const uint32_t pt = p + i % T::kPBufs * T::kP + k * 256;
-          tc_product(tmem + 2 * NT, operand(at, D == 128 ? kTok * 128 : 0, 1024, 2),
-                     operand(pt, 128, 2048, 0), kValues, i > 0 || k > 0);
+          const uint32_t pt = smem_addr(ps) + i % T::kPBufs * T::kP;
+#pragma unroll
+          for (int k = 0; k < kTok / 16; ++k)
+            tc_product(tmem + 2 * NT, operand(at + k * 2048, D == 128 ? kTok * 128 : 0, 1024, 2),
+                       operand(pt + k * 256, 128, 2048, 0), kValues, i > 0 || k > 0);
+          tc_commit(&bars->pv_done[b]);
         }
-        tc_commit(&bars->empty[slot]);
-        tc_commit(&bars->pv_done[i & 1]);
-        if (i + 2 < tiles) ok = scores(i + 2);
       }
-      if (!ok) {  // given up: let what was issued end before tensor memory is freed
-        tc_commit(&bars->drained);
-        mbar_wait_bounded(&bars->drained, 0);
+      __syncwarp();
+      if (loaded < tiles) {  // the stage is free once the product that reads it is done
+        ok = wait_or_give_up(keys ? &bars->s_full[b] : &bars->pv_done[b], phase, gave_up);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        load();
       }
     }
-  } else if (warp < 4) {
+    if (!kTma) copy_wait_all();
+    if (*gave_up) {  // let what was issued end before tensor memory is freed
+      if (lane == 0) tc_commit(&bars->drained[warp - 4]);
+      mbar_wait_bounded(&bars->drained[warp - 4], 0);
+    }
+  } else if (tiles > 0) {
     // ---- softmax: one thread per position of the tile
     const uint32_t lanes = (uint32_t)warp << 21;  // this warp's 32 lanes of tensor memory
-    for (int i = tid; i < NT * D / 8; i += kSoft) {
-      const int r = i / (D / 8), c = i % (D / 8), pr = row0 + r;
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (pr < rows)
-        x = *reinterpret_cast<const uint4 *>(
-            static_cast<const uint16_t *>(a.q) +
-            ((int64_t)n * a.R + pr / G) * a.q_row_stride + (int64_t)(h * G + pr % G) * a.q_head_stride +
-            c * 8);
-      *reinterpret_cast<uint4 *>(qs + c / 8 * (NT * 128) + r * 128 + ((c % 8) ^ (r % 8)) * 16) = x;
+    {
+      constexpr int kMine = NT * D / 8 / kSoft;
+      uint4 x[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int r = (tid + i * kSoft) / (D / 8), c = (tid + i * kSoft) % (D / 8), pr = row0 + r;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (pr < rows)
+          x[i] = *reinterpret_cast<const uint4 *>(
+              static_cast<const uint16_t *>(a.q) + ((int64_t)n * a.R + pr / G) * a.q_row_stride +
+              (int64_t)(h * G + pr % G) * a.q_head_stride + c * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int r = (tid + i * kSoft) / (D / 8), c = (tid + i * kSoft) % (D / 8);
+        *reinterpret_cast<uint4 *>(qs + c / 8 * (NT * 128) + r * 128 + ((c % 8) ^ (r % 8)) * 16) =
+            x[i];
+      }
     }
     fence_async_shared();
     mbar_arrive(&bars->q_full);
@@ -312,13 +325,19 @@ __global__ void __launch_bounds__(TcShape<NT, D, kTma>::kThreads, 2)
     if (a.dev_status && (bad_page || (want > cap && tid == 0)))
       atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
     bad_page = named_or(1, kSoft, bad_page);
-    for (int j = tid; j < NT && row0 + j < rows; j += kSoft) {
-      int r = (row0 + j) / G;
-      if (!parents) {
-        for (int x = 0; x <= r; ++x) atomicOr(desc + x * T::kMaskWords + j / 32, 1u << (j % 32));
-      } else if (row_depth(parents, r) >= 0) {
+    if (!parents) {  // a chain: position x is seen by the rows from x * G on
+      for (int i = tid; i < a.R * T::kMaskWords; i += kSoft) {
+        const int w = i % T::kMaskWords, first = i / T::kMaskWords * G - row0 - w * 32;
+        const int last = rows - row0 - w * 32;  // rows past the block see nothing
+        const uint32_t from = first <= 0 ? 0xFFFFFFFFu : first >= 32 ? 0u : 0xFFFFFFFFu << first;
+        const uint32_t to = last >= 32 ? 0xFFFFFFFFu : last <= 0 ? 0u : (1u << last) - 1u;
+        desc[i] = from & to;
+      }
+    } else if (tid < NT && row0 + tid < rows) {
+      int r = (row0 + tid) / G;
+      if (row_depth(parents, r) >= 0) {
         for (;;) {
-          atomicOr(desc + r * T::kMaskWords + j / 32, 1u << (j % 32));
+          atomicOr(desc + r * T::kMaskWords + tid / 32, 1u << (tid % 32));
           if (r == 0) break;
           r = parents[r - 1] + 1;
         }
@@ -443,18 +462,18 @@ __global__ void __launch_bounds__(TcShape<NT, D, kTma>::kThreads, 2)
       }
       if (masked && !there) {
         // what lies here is no value of the sequence: 0 * NaN is not 0
-        const int item = 2 * i + 1, slot = item % T::kStages;
-        wait_or_give_up(&bars->full[slot], (item / T::kStages) & 1, gave_up);
-        uint8_t *v = ring + slot * T::kTile + tid * 128;
+        const int slot = i % T::kVStages;
+        wait_or_give_up(&bars->v_full[slot], (i / T::kVStages) & 1, gave_up);
+        uint8_t *v = vring + slot * T::kTile + tid * 128;
         for (int c = 0; c < D / 8; ++c)
           *reinterpret_cast<uint4 *>(v + c / 8 * (kTok * 128) + c % 8 * 16) = make_uint4(0, 0, 0, 0);
       }
       if (a.R > 1 && there && t >= len) {
         // 0 * inf is not 0: a value of the block that some rows must not see
         // is taken out here if it is not finite, and added at the end
-        const int item = 2 * i + 1, slot = item % T::kStages;
-        wait_or_give_up(&bars->full[slot], (item / T::kStages) & 1, gave_up);
-        uint8_t *v = ring + slot * T::kTile + tid * 128;
+        const int slot = i % T::kVStages;
+        wait_or_give_up(&bars->v_full[slot], (i / T::kVStages) & 1, gave_up);
+        uint8_t *v = vring + slot * T::kTile + tid * 128;
         bool fix = false;
         for (int c = 0; c < D / 8; ++c) {
           uint16_t *at = reinterpret_cast<uint16_t *>(v + c / 8 * (kTok * 128) +
@@ -497,23 +516,24 @@ __global__ void __launch_bounds__(TcShape<NT, D, kTma>::kThreads, 2)
     }
     named_sync(1, kSoft);
     if (tid < NT) {
-      const int pr = row0 + tid;
       // the root's bits: the rows that belong to the block
-      const bool live = pr < rows && ((desc[tid / 32] >> (tid % 32)) & 1u);
+      const bool live = row0 + tid < rows && ((desc[tid / 32] >> (tid % 32)) & 1u);
       const float s = !live ? 0.f
                             : wred[tid] + wred[NT + tid] + wred[2 * NT + tid] + wred[3 * NT + tid];
       sums[tid] = s;
-      if (pr < rows) {
-        const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
+      facs[tid] = s == 0.f ? 0.f : 1.f / s;
+      if (row0 + tid < rows) {
         if (a.splits > 1)
-          a.part_ml[row * a.splits + split] = make_float2(s == 0.f ? kMinusInf : -nrefs[tid], s);
+          a.part_ml[out_row[tid] * a.splits + split] =
+              make_float2(s == 0.f ? kMinusInf : -nrefs[tid], s);
         else if (a.out_lse)
-          a.out_lse[row] = s == 0.f ? kMinusInf : -nrefs[tid] * kLn2 + logf(s);
+          a.out_lse[out_row[tid]] = s == 0.f ? kMinusInf : -nrefs[tid] * kLn2 + logf(s);
       }
     }
     named_sync(1, kSoft);
     const int d = tid;  // O^T: one thread per element of the head
     const bool fix = bars->fix;
+    uint16_t *staged = reinterpret_cast<uint16_t *>(qs);  // (Q has been read)
 #pragma unroll 1
     for (int c = 0; c < NT && row0 + c < rows; c += 16) {
       float o[16];
@@ -527,29 +547,35 @@ __global__ void __launch_bounds__(TcShape<NT, D, kTma>::kThreads, 2)
           const uint16_t v =
               static_cast<const uint16_t *>(a.v)[off + (int64_t)h * a.g.head_stride + d];
           // (times its weight it is what it is)
-          for (int j = 0; not_finite(v) && j < 16; ++j)
-            if ((desc[x * T::kMaskWords + (c + j) / 32] >> ((c + j) % 32)) & 1u)
-              o[j] += Elem<uint16_t>::to_float(v);
+          const uint32_t seers = desc[x * T::kMaskWords + c / 32] >> (c % 32);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (not_finite(v) && ((seers >> j) & 1u)) o[j] += Elem<uint16_t>::to_float(v);
         }
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        const int pr = row0 + c + j;
-        if (pr >= rows) break;
-        const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
-        const float s = sums[c + j];
-        if (a.splits > 1) {
-          if (s != 0.f) a.part_o[(row * a.splits + split) * D + d] = o[j];
-        } else {
-          static_cast<__nv_bfloat16 *>(a.out_o)[row * D + d] =
-              __float2bfloat16(s == 0.f ? 0.f : o[j] / s);
-        }
+        const bool any = sums[c + j] != 0.f;
+        if (a.splits == 1)
+          staged[(c + j) * D + d] =
+              __bfloat16_as_ushort(__float2bfloat16(any ? o[j] * facs[c + j] : 0.f));
+        else if (any && row0 + c + j < rows)
+          a.part_o[(out_row[c + j] * a.splits + split) * D + d] = o[j];
+      }
+    }
+    if (a.splits == 1) {
+      named_sync(1, kSoft);
+      for (int i = tid; i < NT * D / 8; i += kSoft) {
+        const int j = i / (D / 8), c = i % (D / 8) * 8;
+        if (row0 + j < rows)
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out_o) + out_row[j] * D + c) =
+              *reinterpret_cast<const uint4 *>(staged + j * D + c);
       }
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == 4) {
     tc_fence_after();
     tmem_free(tmem, T::kCols);
   }
@@ -599,7 +625,7 @@ cudaError_t launch_shape(const AttendArgs &a, int32_t row_tiles, int64_t ctas, c
   if (e != cudaSuccess) return e;
   CUtensorMap kmap = {}, vmap = {};
   if (kTma && (!pool_map(&kmap, a, a.k) || !pool_map(&vmap, a, a.v))) return cudaErrorInvalidValue;
-  return launch_pdl(attend_tc_kernel<NT, D, kTma>, dim3((unsigned)ctas), dim3(T::kThreads),
+  return launch_pdl(attend_tc_kernel<NT, D, kTma>, dim3((unsigned)ctas), dim3(kTcThreads),
                     T::kSmem, stream, kmap, vmap, a, row_tiles);
 }
 

@@ -120,6 +120,10 @@ __device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // ---- arithmetic on pairs ------------------------------------------------------------
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   uint64_t d;
@@ -146,17 +150,22 @@ __device__ __forceinline__ float warp_max_f32(float v) {
 
 // ---- waits --------------------------------------------------------------------------
 // Waits for a phase unless the CTA gave up already; gives up after ~2 s and
-// tells the rest of the CTA.
+// tells the rest of the CTA.  (The clock is read now and then only: a read
+// costs more than many tests.)
 __device__ __forceinline__ bool wait_or_give_up(uint64_t *bar, uint32_t parity,
                                                 volatile uint32_t *gave_up) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (*gave_up) return false;
-    if (global_timer_ns() - t0 > 2000000000ull) {
-      *gave_up = 1;
-      return false;
+  if (mbar_test(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t k = 1;; ++k) {
+    if (mbar_test(bar, parity)) return true;
+    if (k % 1024 == 0) {
+      if (*gave_up) return false;
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > 2000000000ull) {
+        *gave_up = 1;
+        return false;
+      }
     }
   }
 }
