@@ -42,6 +42,8 @@ constexpr int kSoft = 128;  // softmax threads
 constexpr int kTcThreads = kSoft + 64;
 constexpr float kUnset = -1e30f;   // no reference yet
 constexpr float kHeadroom = 60.f;  // log2 units a score may exceed its reference by
+constexpr float kFar = 1.152921504606847e18f;     // 2^kHeadroom
+constexpr float kForget = 7.52316384526264e-37f;  // 2^-120
 constexpr float kMinusInf = -INFINITY;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kSmemPerCta = 113 * 1024;  // two CTAs per SM
@@ -53,7 +55,7 @@ struct TcShape {
   static constexpr int kP = NT * kTok * 2;
   static constexpr int kPBufs = NT <= 48 ? 2 : 1;
   static constexpr int kMaskWords = (NT + 31) / 32;
-  static constexpr int kSmall = PSI_MAX_BLOCK_ROWS * kMaskWords * 4 + 9 * NT * 4 + 512;
+  static constexpr int kSmall = PSI_MAX_BLOCK_ROWS * kMaskWords * 4 + 8 * NT * 4 + 512;
   static constexpr int kRoom = (kSmemPerCta - 1024 - kSmall - kQ - kPBufs * kP) / kTile;
   static constexpr int kStages = kRoom < 6 ? kRoom : 6;
   static constexpr int kKStages = (kStages + 1) / 2, kVStages = kStages / 2;
@@ -70,46 +72,61 @@ struct TcBarriers {
 
 __device__ __forceinline__ bool not_finite(uint16_t b) { return (b & 0x7F80u) == 0x7F80u; }
 
-// x[0..15] = scores of packed rows c.. of this thread's position above their
-// references, in log2 units (-inf where a row does not see it); returns the
-// largest of them and `top`.
-template <bool kMasked>
-__device__ __forceinline__ float above(const float s[16], float scale2, const float *nrefs,
-                                       uint32_t seen, float top, float x[16]) {
+// Weights of 16 packed rows at this thread's position: w = 2^(score - ref)
+// (0 where a row does not see it), packed as bf16 pairs and added to the
+// rows' sums; `all` gathers them to show whether a score is far above its
+// reference.  kAgain: the references were raised by factors of facs, in which
+// the sums, which may hold these weights already, are rescaled; a row raised
+// by more than 2^120 keeps nothing of what it had (at most 2^-40 of the new).
+template <bool kMasked, bool kAgain>
+__device__ __forceinline__ void weigh(const float s[16], float scale2, const float *nrefs,
+                                      const float *facs, uint32_t seen, float l[16], float2 &all,
+                                      uint32_t packed[8]) {
 #pragma unroll
   for (int j = 0; j < 16; j += 4) {
     const float4 r = *reinterpret_cast<const float4 *>(nrefs + j);
     const float2 k = make_float2(scale2, scale2);
-    const float2 a = fma2(make_float2(s[j], s[j + 1]), k, make_float2(r.x, r.y));
-    const float2 b = fma2(make_float2(s[j + 2], s[j + 3]), k, make_float2(r.z, r.w));
-    x[j] = a.x;
-    x[j + 1] = a.y;
-    x[j + 2] = b.x;
-    x[j + 3] = b.y;
-  }
-  if (kMasked) {
+    float2 x[2] = {fma2(make_float2(s[j], s[j + 1]), k, make_float2(r.x, r.y)),
+                   fma2(make_float2(s[j + 2], s[j + 3]), k, make_float2(r.z, r.w))};
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = (seen >> j) & 1u ? x[j] : kMinusInf;
+    for (int h = 0; h < 2; ++h) {
+      const int q = j + 2 * h;
+      if (kMasked) {
+        x[h].x = (seen >> q) & 1u ? x[h].x : kMinusInf;
+        x[h].y = (seen >> (q + 1)) & 1u ? x[h].y : kMinusInf;
+      }
+      const float2 p = make_float2(fast_exp2(x[h].x), fast_exp2(x[h].y));
+      float2 t;
+      if (kAgain) {
+        const float2 f = *reinterpret_cast<const float2 *>(facs + q);
+        t.x = f.x < kForget ? p.x : l[q] * f.x;
+        t.y = f.y < kForget ? p.y : l[q + 1] * f.y;
+      } else {
+        t = add2(make_float2(l[q], l[q + 1]), p);
+        all = add2(all, p);
+      }
+      l[q] = t.x;
+      l[q + 1] = t.y;
+      const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+      packed[q / 2] = *reinterpret_cast<const uint32_t *>(&b);
+    }
   }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) top = fmaxf(top, x[j]);
-  return top;
 }
 
-// 2^x of 16 rows to the sums and, as bf16, to the operand P^T.
-__device__ __forceinline__ void weights(float x[16], float *l, uint8_t *pt) {
-  uint32_t w[8];
+// 16 values of each lane reduced over the warp: lane x returns value x % 16.
+template <typename Op>
+__device__ __forceinline__ float reduce16(float v[16], Op op) {
+  const int lane = threadIdx.x % 32;
 #pragma unroll
-  for (int j = 0; j < 16; j += 2) {
-    const float2 p = make_float2(fast_exp2(x[j]), fast_exp2(x[j + 1]));
-    const float2 t = add2(make_float2(l[j], l[j + 1]), p);
-    l[j] = t.x;
-    l[j + 1] = t.y;
-    const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
-    w[j / 2] = *reinterpret_cast<const uint32_t *>(&b);
+  for (int w = 8; w > 0; w /= 2) {
+#pragma unroll
+    for (int j = 0; j < w; ++j) {
+      const bool up = lane & w;
+      const float keep = up ? v[j + w] : v[j], give = up ? v[j] : v[j + w];
+      v[j] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, give, w));
+    }
   }
-  *reinterpret_cast<uint4 *>(pt) = make_uint4(w[0], w[1], w[2], w[3]);
-  *reinterpret_cast<uint4 *>(pt + 2048) = make_uint4(w[4], w[5], w[6], w[7]);
+  return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 16));
 }
 
 template <int NT, int D, bool kTma>
@@ -125,8 +142,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   uint32_t *desc = reinterpret_cast<uint32_t *>(ps + T::kPBufs * T::kP);  // [R][kMaskWords]
   float *nrefs = reinterpret_cast<float *>(desc + PSI_MAX_BLOCK_ROWS * T::kMaskWords);  // [NT]
   float *facs = nrefs + NT;                                                             // [NT]
-  float *sums = facs + NT;                                                              // [NT]
-  float *wred = sums + NT;                                                              // [4][NT]
+  float *wred = facs + NT;                                                              // [4][NT]
   int64_t *out_row = reinterpret_cast<int64_t *>(wred + 4 * NT);                        // [NT]
   TcBarriers *bars = reinterpret_cast<TcBarriers *>(out_row + NT);
   static_assert(sizeof(TcBarriers) <= 512, "");
@@ -350,15 +366,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     float l[NT];  // sums of this thread's positions
 #pragma unroll
     for (int j = 0; j < NT; ++j) l[j] = 0.f;
-    // with few rows a tile's scores stay in registers between the two steps
-    constexpr bool kKeep = NT <= 48;
-    float kept[kKeep ? NT : 1];
     for (int i = 0; i < tiles; ++i) {
       const int t = begin + i * kTok + tid;
       // rows that see this thread's position
       uint32_t seen[T::kMaskWords];
       const bool masked = begin + (i + 1) * kTok > (len < end ? len : end) || bad_page;
       bool there = true;
+#pragma unroll
+      for (int w = 0; w < T::kMaskWords; ++w) seen[w] = 0xFFFFFFFFu;
       if (masked) {
         there = t < end && page_of(a.g, table, t) >= 0;
 #pragma unroll
@@ -370,42 +385,43 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       __syncwarp();
       tc_fence_after();
       const uint32_t st = tmem + lanes + (i & 1) * NT;
-      // how far scores exceed their references
-      const auto exceed = [&](auto mask) {
-        float top = kMinusInf;
-        if constexpr (kKeep) {
+      uint32_t packed[NT / 2];
+      const auto weigh_tile = [&](auto mask, auto again) {
+        float2 all = make_float2(0.f, 0.f);
+        float s[2][16];
+        tmem_ld16(st, s[0]);
 #pragma unroll
-          for (int c = 0; c < NT; c += 16) tmem_ld16(st + c, kept + c);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < NT; c += 16)
-            top = above<mask.value>(kept + c, a.scale2, nrefs + c, seen[c / 32] >> (c % 32), top,
-                                    kept + c);
-        } else {
-#pragma unroll
-          for (int c = 0; c < NT; c += 16) {
-            float s[16];
-            tmem_ld16(st + c, s);
-            tmem_wait_ld();
-            top = above<mask.value>(s, a.scale2, nrefs + c, seen[c / 32] >> (c % 32), top, s);
-          }
+        for (int c = 0; c < NT; c += 16) {
+          const int b = c / 16 % 2;
+          tmem_wait_ld16(s[b]);
+          if (c + 16 < NT) tmem_ld16(st + c + 16, s[1 - b]);
+          weigh<mask.value, again.value>(s[b], a.scale2, nrefs + c, facs + c,
+                                         seen[c / 32] >> (c % 32), l + c, all, packed + c / 2);
         }
-        return top;
+        return all.x + all.y;
       };
-      const float top = masked ? exceed(std::true_type{}) : exceed(std::false_type{});
-      if (named_or(1, kSoft, top > kHeadroom)) {
-        // raise those references to the tile's maxima and rescale what is there
-#pragma unroll
+      using std::false_type;
+      using std::true_type;
+      // the first tile sets the references; later ones seldom raise them
+      bool raise = i == 0;
+      if (!raise) {
+        const float all = masked ? weigh_tile(true_type{}, false_type{})
+                                 : weigh_tile(false_type{}, false_type{});
+        raise = named_or(1, kSoft, !(all <= kFar));
+      }
+      if (raise) {
+#pragma unroll 1
         for (int c = 0; c < NT; c += 16) {
           float s[16];
           tmem_ld16(st + c, s);
-          tmem_wait_ld();
+          tmem_wait_ld16(s);
+          constexpr int kLast = T::kMaskWords - 1;
+          const uint32_t word = c < 32 ? seen[0] : c < 64 ? seen[kLast < 1 ? kLast : 1] : seen[kLast];
+          const uint32_t sees = word >> (c % 32);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const bool sees = !masked || ((seen[(c + j) / 32] >> ((c + j) % 32)) & 1u);
-            const float m = warp_max_f32(sees ? s[j] * a.scale2 : kMinusInf);
-            if (lane == 0) wred[warp * NT + c + j] = m;
-          }
+          for (int j = 0; j < 16; ++j) s[j] = (sees >> j) & 1u ? s[j] * a.scale2 : kMinusInf;
+          const float m = reduce16(s, [](float x, float y) { return fmaxf(x, y); });
+          if (lane < 16) wred[warp * NT + c + lane] = m;
         }
         named_sync(1, kSoft);
         if (tid < NT) {
@@ -413,30 +429,25 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                 fmaxf(wred[2 * NT + tid], wred[3 * NT + tid]));
           // (each row by its own scores: what other rows see does not touch its bits)
           const float old = -nrefs[tid], now = m > old + kHeadroom ? m : old;
-          facs[tid] = fast_exp2(old - now);
+          facs[tid] = now == old && i > 0 ? 1.f : fast_exp2(old - now);
           nrefs[tid] = -now;
         }
         if (i > 0) wait_or_give_up(&bars->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
         named_sync(1, kSoft);
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < NT; c += 16) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) l[c + j] *= facs[c + j];
-          if (i > 0) {
+        if (i > 0) {
+#pragma unroll 1
+          for (int c = 0; c < NT; c += 16) {
             float o[16];
             tmem_ld16(tmem + lanes + 2 * NT + c, o);
-            tmem_wait_ld();
+            tmem_wait_ld16(o);
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] *= facs[c + j];
             tmem_st16(tmem + lanes + 2 * NT + c, o);
           }
+          tmem_wait_st();
         }
-        tmem_wait_st();
-        if constexpr (kKeep) {
-          if (masked) exceed(std::true_type{});
-          else exceed(std::false_type{});
-        }
+        weigh_tile(true_type{}, true_type{});
       }
       // the buffer of P^T is free once its last product is done
       if (i >= T::kPBufs) {
@@ -446,20 +457,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
       uint8_t *pt = ps + i % T::kPBufs * T::kP + tid / 8 * 128 + tid % 8 * 16;
 #pragma unroll
-      for (int c = 0; c < NT; c += 16) {
-        if constexpr (kKeep) {
-          weights(kept + c, l + c, pt + c / 8 * 2048);
-        } else {
-          float s[16];
-          tmem_ld16(st + c, s);
-          tmem_wait_ld();
-          if (masked)
-            above<true>(s, a.scale2, nrefs + c, seen[c / 32] >> (c % 32), 0.f, s);
-          else
-            above<false>(s, a.scale2, nrefs + c, 0u, 0.f, s);
-          weights(s, l + c, pt + c / 8 * 2048);
-        }
-      }
+      for (int c = 0; c < NT / 2; c += 4)
+        *reinterpret_cast<uint4 *>(pt + c / 4 * 2048) =
+            make_uint4(packed[c], packed[c + 1], packed[c + 2], packed[c + 3]);
       if (masked && !there) {
         // what lies here is no value of the sequence: 0 * NaN is not 0
         const int slot = i % T::kVStages;
@@ -500,19 +500,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __syncwarp();
     tc_fence_after();
 #pragma unroll
-    for (int c = 0; c < NT; c += 16) {  // add up the lanes: lane x ends with row c + x % 16
-      float *v = l + c;
-#pragma unroll
-      for (int w = 8; w > 0; w /= 2) {
-#pragma unroll
-        for (int j = 0; j < w; ++j) {
-          const bool up = lane & w;
-          const float keep = up ? v[j + w] : v[j], give = up ? v[j] : v[j + w];
-          v[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, w);
-        }
-      }
-      v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], 16);
-      if (lane < 16) wred[warp * NT + c + lane] = v[0];
+    for (int c = 0; c < NT; c += 16) {  // add up the lanes
+      const float sum = reduce16(l + c, [](float x, float y) { return x + y; });
+      if (lane < 16) wred[warp * NT + c + lane] = sum;
     }
     named_sync(1, kSoft);
     if (tid < NT) {
@@ -520,7 +510,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const bool live = row0 + tid < rows && ((desc[tid / 32] >> (tid % 32)) & 1u);
       const float s = !live ? 0.f
                             : wred[tid] + wred[NT + tid] + wred[2 * NT + tid] + wred[3 * NT + tid];
-      sums[tid] = s;
       facs[tid] = s == 0.f ? 0.f : 1.f / s;
       if (row0 + tid < rows) {
         if (a.splits > 1)
@@ -538,7 +527,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     for (int c = 0; c < NT && row0 + c < rows; c += 16) {
       float o[16];
       tmem_ld16(tmem + lanes + 2 * NT + c, o);
-      tmem_wait_ld();
+      tmem_wait_ld16(o);
       if (d >= D) continue;
       if (fix) {
         for (int x = 0; x < a.R; ++x) {
@@ -553,14 +542,24 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             if (not_finite(v) && ((seers >> j) & 1u)) o[j] += Elem<uint16_t>::to_float(v);
         }
       }
+      float f[16];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const bool any = sums[c + j] != 0.f;
-        if (a.splits == 1)
-          staged[(c + j) * D + d] =
-              __bfloat16_as_ushort(__float2bfloat16(any ? o[j] * facs[c + j] : 0.f));
-        else if (any && row0 + c + j < rows)
-          a.part_o[(out_row[c + j] * a.splits + split) * D + d] = o[j];
+      for (int j = 0; j < 16; j += 4)
+        *reinterpret_cast<float4 *>(f + j) = *reinterpret_cast<const float4 *>(facs + c + j);
+      if (a.splits == 1) {
+        uint16_t b[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)  // (a row that sees nothing: 0 whatever the others saw)
+          b[j] = __bfloat16_as_ushort(__float2bfloat16(f[j] == 0.f ? 0.f : o[j] * f[j]));
+#pragma unroll
+        for (int j = 0; j < 16; ++j) staged[(c + j) * D + d] = b[j];
+      } else {
+        int64_t at[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) at[j] = out_row[c + j];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (row0 + c + j < rows) a.part_o[(at[j] * a.splits + split) * D + d] = o[j];
       }
     }
     if (a.splits == 1) {
