@@ -67,13 +67,12 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   __shared__ uint32_t sees[kRowTile][kBlockWords];
   __shared__ int64_t offs[kTokTile];
 
-  int64_t id = blockIdx.x;
-  const int split = (int)(id % a.splits);
-  id /= a.splits;
-  const int tile = (int)(id % row_tiles);
+  int id = blockIdx.x;
+  const int tile = id % row_tiles;
   id /= row_tiles;
-  const int h = (int)(id % a.kv_heads);
-  const int n = (int)(id / a.kv_heads);
+  const int h = id % a.kv_heads;
+  id /= a.kv_heads;
+  const int n = id % a.N, split = id / a.N;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_wait();
   const int len = a.g.lens[n];
@@ -84,6 +83,10 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   const int64_t cap = table_capacity(a.g);
   const int64_t want = (int64_t)len + a.R;
   const int T = (int)(want < cap ? want : cap);
+  const Ranges range = deal(T, a.splits, a.least);
+  if (split >= range.units) return;
+  const int begin = split * range.per;
+  const int end = T - begin < range.per ? T : begin + range.per;
   if (want > cap && a.dev_status && tid == 0) atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
 
   for (int i = tid; i < kRowTile; i += kSimtThreads) {
@@ -105,9 +108,6 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   }
   __syncthreads();
 
-  const int per = ((T + a.splits - 1) / a.splits + kTokTile - 1) / kTokTile * kTokTile;
-  const int begin = split * per < T ? split * per : T;
-  const int end = begin + per < T ? begin + per : T;
   float m[4], l[4], acc[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
     const int pr = tile * kRowTile + warp * 4 + i;
     if (pr >= rows) continue;
     const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
-    if (a.splits > 1) {
+    if (range.units > 1) {
       const int64_t at = row * a.splits + split;
       if (lane == 0) a.part_ml[at] = make_float2(m[i], l[i]);
 #pragma unroll
@@ -228,38 +228,58 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   }
 }
 
-// Adds up the partial results of one output row, in the order of the splits:
-// one warp per row.
+// Adds up the partial results of one output row, in the order of the ranges:
+// one CTA per row, the ranges' elements eight loads at a time.
+constexpr int kJoinThreads = 128;
+constexpr int kMaxSplits = 256;
 template <typename Bits>
-__global__ void __launch_bounds__(128) join_kernel(AttendArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (row >= (int64_t)a.N * a.R * a.q_heads) return;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
+  __shared__ float weight[kMaxSplits], top_l[2];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid % 32;
   pdl_wait();
-  if (a.g.lens[row / ((int64_t)a.R * a.q_heads)] < 0) return;
-  const float2 *ml = a.part_ml + row * a.splits;
-  float top = kNegInf;
-  bool any = false;
-  for (int s = 0; s < a.splits; ++s) {
-    top = fmaxf(top, ml[s].x);
-    any |= ml[s].y != 0.f;
-  }
-  float l = 0.f, acc[8] = {};
-  for (int s = 0; any && s < a.splits; ++s) {
-    if (ml[s].y == 0.f) continue;
-    const float w = fast_exp2(ml[s].x - top);
-    l = fmaf(w, ml[s].y, l);
-    const float *o = a.part_o + (row * a.splits + s) * a.D;
+  const int len = a.g.lens[row / ((int64_t)a.R * a.q_heads)];
+  if (len < 0) return;
+  const int64_t cap = table_capacity(a.g), want = (int64_t)len + a.R;
+  const int units = deal((int)(want < cap ? want : cap), a.splits, a.least).units;
+  if (units == 1) return;  // (the row is written already)
+  if (tid < 32) {
+    const float2 *ml = a.part_ml + row * a.splits;
+    float2 mine[kMaxSplits / 32];
+    float top = kNegInf, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k * 32 + lane < a.D) acc[k] = fmaf(w, o[k * 32 + lane], acc[k]);
-  }
-  if (lane == 0 && a.out_lse)
-    a.out_lse[row] = any ? top * kLn2 + logf(l) : kNegInf;
+    for (int k = 0; k < kMaxSplits / 32; ++k) {
+      mine[k] = k * 32 + lane < units ? ml[k * 32 + lane] : make_float2(kNegInf, 0.f);
+      if (mine[k].y != 0.f) top = fmaxf(top, mine[k].x);
+    }
+    top = warp_max(top);
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k * 32 + lane < a.D)
-      Store<Bits>::put(a.out_o, row * a.D + k * 32 + lane, any ? acc[k] / l : 0.f);
+    for (int k = 0; k < kMaxSplits / 32; ++k) {
+      const float w = mine[k].y != 0.f ? fast_exp2(mine[k].x - top) : 0.f;
+      if (k * 32 < units) weight[k * 32 + lane] = w;
+      if (mine[k].y != 0.f) l = fmaf(w, mine[k].y, l);
+    }
+    l = warp_sum(l);
+    if (lane == 0) {
+      top_l[0] = l;
+      if (a.out_lse) a.out_lse[row] = l != 0.f ? top * kLn2 + logf(l) : kNegInf;
+    }
+  }
+  __syncthreads();
+  const float l = top_l[0];
+  for (int d = tid; d < a.D; d += kJoinThreads) {
+    const float *o = a.part_o + row * a.splits * a.D + d;
+    float acc = 0.f;
+    for (int s0 = 0; s0 < units; s0 += 8) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = s0 + k < units ? o[(int64_t)(s0 + k) * a.D] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)  // (a range without weight left nothing to read)
+        if (s0 + k < units && weight[s0 + k] != 0.f) acc = fmaf(weight[s0 + k], v[k], acc);
+    }
+    Store<Bits>::put(a.out_o, row * a.D + d, l != 0.f ? acc / l : 0.f);
+  }
 }
 
 size_t simt_smem(int D) {
@@ -282,7 +302,7 @@ cudaError_t launch_simt(const AttendArgs &a, const AttendPlan &plan, cudaStream_
 template <typename Bits>
 cudaError_t launch_join(const AttendArgs &a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.N * a.R * a.q_heads;
-  return launch_pdl(join_kernel<Bits>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a);
+  return launch_pdl(join_kernel<Bits>, dim3((unsigned)rows), dim3(kJoinThreads), 0, stream, a);
 }
 
 }  // namespace
@@ -295,10 +315,16 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
   p.rows = p.tc ? attend_tc_rows(rows) : kRowTile;
   p.row_tiles = (rows + p.rows - 1) / p.rows;
   const int64_t base = (int64_t)N * kv_heads * p.row_tiles;
-  // CTAs that the device holds at once; a range is worth a CTA from 256 positions
+  // CTAs that the device holds at once.  A short batch is dealt out to about
+  // two of them each; a long one in ranges of at least 8 tiles, a quarter of
+  // an SM's share each, so that ragged lengths even out.  The table's width
+  // bounds the lengths; shorter sequences get shorter ranges (`least`).
   const int64_t fill = (int64_t)device_sm_count() * (p.tc ? 2 : 4);
-  const int64_t most = std::max<int64_t>(1, capacity / 256);
-  p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({fill / base, most, 128}));
+  const int64_t tiles = (capacity + kPosTile - 1) / kPosTile;
+  const auto share = [&](int64_t waves) { return (tiles * base + waves * fill - 1) / (waves * fill); };
+  const int64_t per = share(2) <= 8 ? std::max<int64_t>(share(2), 1) : std::max<int64_t>(share(4), 8);
+  p.least = (int32_t)std::min<int64_t>(8, (16 * base + fill - 1) / fill);
+  p.splits = (int32_t)std::min<int64_t>((tiles + per - 1) / per, kMaxSplits);
   p.ctas = base * p.splits;
   const size_t parts = (size_t)N * R * q_heads * p.splits;
   p.workspace = p.splits > 1 ? parts * (sizeof(float) * D + sizeof(float2)) : 0;
@@ -308,6 +334,7 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
 cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan, void *workspace,
                           cudaStream_t stream) {
   a.splits = plan.splits;
+  a.least = plan.least;
   if (plan.ctas > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   const size_t parts = (size_t)a.N * a.R * a.q_heads * plan.splits;
   a.part_o = static_cast<float *>(workspace);

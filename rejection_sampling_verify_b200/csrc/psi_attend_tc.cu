@@ -37,7 +37,7 @@
 namespace psi {
 namespace {
 
-constexpr int kTok = 128;   // positions per tile
+constexpr int kTok = kPosTile;  // positions per tile
 constexpr int kSoft = 128;  // softmax threads
 constexpr int kTcThreads = kSoft + 64;
 constexpr float kUnset = -1e30f;   // no reference yet
@@ -172,13 +172,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   }
   pdl_wait();
 
+  // full ranges come first, the ends of the longest sequences last
   int id = blockIdx.x;
-  const int split = id % a.splits;
-  id /= a.splits;
   const int row0 = id % row_tiles * NT;
   id /= row_tiles;
   const int h = id % a.kv_heads;
-  const int n = id / a.kv_heads;
+  id /= a.kv_heads;
+  const int n = id % a.N, split = id / a.N;
   const int len = a.g.lens[n];
   const int G = a.q_heads / a.kv_heads;
   const int rows = a.R * G;
@@ -186,10 +186,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
   const int64_t cap = table_capacity(a.g), want = (int64_t)len + a.R;
   const int total = len < 0 ? 0 : (int)(want < cap ? want : cap);  // 0: the sequence is not there
-  const int per = ((total + a.splits - 1) / a.splits + kTok - 1) / kTok * kTok;
-  const int begin = split * per < total ? split * per : total;
-  const int end = begin + per < total ? begin + per : total;
-  const int tiles = (end - begin + kTok - 1) / kTok;
+  const Ranges range = total > 0 ? deal(total, a.splits, a.least) : Ranges{0, 0};
+  const bool joined = range.units > 1;
+  const int begin = split < range.units ? split * range.per : total;
+  const int end = total - begin < range.per ? total : begin + range.per;
+  const int tiles = (end - begin + kTok - 1) / kTok;  // 0: nothing for this CTA
   if (tid < NT) {  // where the packed rows go
     const int pr = row0 + tid;
     out_row[tid] = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
@@ -197,8 +198,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   __syncthreads();
   const uint32_t tmem = bars->tmem;
   volatile uint32_t *gave_up = &bars->gave_up;
-  if (tiles == 0 && len >= 0 && tid < NT && row0 + tid < rows)
-    a.part_ml[out_row[tid] * a.splits + split] = make_float2(kMinusInf, 0.f);  // (only when split)
 
   if (tiles > 0 && (warp == 4 || warp == 5)) {
     // ---- loads and products of keys (warp 4) or values (warp 5)
@@ -512,7 +511,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                             : wred[tid] + wred[NT + tid] + wred[2 * NT + tid] + wred[3 * NT + tid];
       facs[tid] = s == 0.f ? 0.f : 1.f / s;
       if (row0 + tid < rows) {
-        if (a.splits > 1)
+        if (joined)
           a.part_ml[out_row[tid] * a.splits + split] =
               make_float2(s == 0.f ? kMinusInf : -nrefs[tid], s);
         else if (a.out_lse)
@@ -546,7 +545,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
       for (int j = 0; j < 16; j += 4)
         *reinterpret_cast<float4 *>(f + j) = *reinterpret_cast<const float4 *>(facs + c + j);
-      if (a.splits == 1) {
+      if (!joined) {
         uint16_t b[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j)  // (a row that sees nothing: 0 whatever the others saw)
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           if (row0 + c + j < rows) a.part_o[(at[j] * a.splits + split) * D + d] = o[j];
       }
     }
-    if (a.splits == 1) {
+    if (!joined) {
       named_sync(1, kSoft);
       for (int i = tid; i < NT * D / 8; i += kSoft) {
         const int j = i / (D / 8), c = i % (D / 8) * 8;

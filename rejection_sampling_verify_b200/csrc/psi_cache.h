@@ -19,8 +19,10 @@ struct AttendArgs {
   void *out_o;
   float *out_lse;
   uint32_t *dev_status;
-  // split over the length: partial results, joined by a second kernel
-  int32_t splits;
+  // a long sequence is dealt to several CTAs: partial results, joined by a
+  // second kernel
+  int32_t splits;  // ranges of a sequence at most
+  int32_t least;   // tiles of a range at least
   float *part_o;   // [N * R * q_heads][splits][D], relative to part_ml's maximum
   float2 *part_ml; // [N * R * q_heads][splits]: maximum (log2 units), sum
   int32_t box;     // positions per TMA box
@@ -28,7 +30,7 @@ struct AttendArgs {
 struct AttendPlan {
   bool tc;        // on the tensor cores
   int32_t rows;   // packed rows per CTA
-  int32_t splits, row_tiles;
+  int32_t splits, least, row_tiles;
   int64_t ctas;
   size_t workspace;
 };

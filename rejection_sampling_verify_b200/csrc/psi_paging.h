@@ -86,6 +86,23 @@ PSI_HD int32_t path_prefix(const int32_t *nodes, int32_t len, int32_t M) {
   return n;
 }
 
+// How a sequence's positions are dealt to the CTAs of its rows: `units`
+// ranges of `per` positions (a multiple of the tile of 128), at most `splits`
+// of them and none below `least` tiles.
+constexpr int kPosTile = 128;
+struct Ranges {
+  int32_t units, per;
+};
+PSI_HD Ranges deal(int32_t total, int32_t splits, int32_t least) {
+  const int32_t tiles = (total - 1) / kPosTile + 1;
+  int32_t per = (tiles - 1) / splits + 1;
+  if (per < least) per = least;
+  Ranges r;
+  r.units = (tiles - 1) / per + 1;
+  r.per = per * kPosTile;
+  return r;
+}
+
 // Pages for `slots` positions.
 PSI_HD int64_t pages_for(int64_t slots, int32_t page_size) {
   return slots <= 0 ? 0 : (slots + page_size - 1) / page_size;
