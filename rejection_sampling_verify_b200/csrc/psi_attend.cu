@@ -312,14 +312,16 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
   AttendPlan p;
   const int rows = R * (q_heads / kv_heads);
   p.tc = attend_tc_fits(dtype, D);
-  p.rows = p.tc ? attend_tc_rows(rows) : kRowTile;
+  p.rows = kRowTile;
+  p.groups = 1;
+  if (p.tc) attend_tc_rows(rows, &p);
   p.row_tiles = (rows + p.rows - 1) / p.rows;
   const int64_t base = (int64_t)N * kv_heads * p.row_tiles;
   // CTAs that the device holds at once.  A short batch is dealt out to about
   // two of them each; a long one in ranges of at least 8 tiles, a quarter of
   // an SM's share each, so that ragged lengths even out.  The table's width
   // bounds the lengths; shorter sequences get shorter ranges (`least`).
-  const int64_t fill = (int64_t)device_sm_count() * (p.tc ? 2 : 4);
+  const int64_t fill = (int64_t)device_sm_count() * (!p.tc ? 4 : p.groups == 1 ? 2 : 1);
   const int64_t tiles = (capacity + kPosTile - 1) / kPosTile;
   const auto share = [&](int64_t waves) { return (tiles * base + waves * fill - 1) / (waves * fill); };
   const int64_t per = share(2) <= 8 ? std::max<int64_t>(share(2), 1) : std::max<int64_t>(share(4), 8);

@@ -22,9 +22,12 @@
 // lane per box); other page sizes gather the rows' 16-byte chunks with
 // asynchronous copies.
 //
-// Warps: 0-3 softmax; 4 loads keys and issues the products K Q^T; 5 loads
-// values and issues V^T P^T.  Keys and values have stages of their own, so
-// that the next keys load while the weights of this tile are at work.
+// Warps: four of softmax for each group of NT rows; one that loads keys and
+// issues the products K Q^T; one that loads values and issues V^T P^T.  Keys
+// and values have stages of their own, so that the next keys load while the
+// weights of this tile are at work.  Up to 80 packed rows make one group, two
+// CTAs to an SM; more make CTAs of two groups, one to an SM, whose products
+// share the tiles of keys and values (twice the work per loaded tile).
 #include <cuda.h>
 #include <math.h>
 
@@ -38,34 +41,40 @@ namespace psi {
 namespace {
 
 constexpr int kTok = kPosTile;  // positions per tile
-constexpr int kSoft = 128;  // softmax threads
-constexpr int kTcThreads = kSoft + 64;
+constexpr int kSoft = 128;  // softmax threads of a group
 constexpr float kUnset = -1e30f;   // no reference yet
 constexpr float kHeadroom = 60.f;  // log2 units a score may exceed its reference by
 constexpr float kFar = 1.152921504606847e18f;     // 2^kHeadroom
 constexpr float kForget = 7.52316384526264e-37f;  // 2^-120
 constexpr float kMinusInf = -INFINITY;
 constexpr float kLn2 = 0.69314718055994531f;
-constexpr int kSmemPerCta = 113 * 1024;  // two CTAs per SM
 
-template <int NT, int D, bool kTma>
+template <int NT, int D, int kGroups>
 struct TcShape {
+  static constexpr int kThreads = kGroups * kSoft + 64;
   static constexpr int kTile = kTok * D * 2;  // bytes of keys or values per stage
-  static constexpr int kQ = NT * D * 2;
+  static constexpr int kQ = NT * D * 2;       // per group, as what follows
   static constexpr int kP = NT * kTok * 2;
   static constexpr int kPBufs = NT <= 48 ? 2 : 1;
   static constexpr int kMaskWords = (NT + 31) / 32;
-  static constexpr int kSmall = PSI_MAX_BLOCK_ROWS * kMaskWords * 4 + 8 * NT * 4 + 512;
-  static constexpr int kRoom = (kSmemPerCta - 1024 - kSmall - kQ - kPBufs * kP) / kTile;
+  static constexpr int kMasks = PSI_MAX_BLOCK_ROWS * kMaskWords * 4;
+  static constexpr int kSmall = kMasks + 8 * NT * 4;
+  static constexpr int kFixed = 1024 + 640 + kGroups * (kQ + kPBufs * kP + kSmall);
+  static constexpr int kRoom = ((kGroups == 1 ? 113 : 227) * 1024 - kFixed) / kTile;
   static constexpr int kStages = kRoom < 6 ? kRoom : 6;
-  static constexpr int kKStages = (kStages + 1) / 2, kVStages = kStages / 2;
-  static constexpr int kSmem = 1024 + kStages * kTile + kQ + kPBufs * kP + kSmall;
-  static constexpr int kCols = 3 * NT <= 64 ? 64 : 3 * NT <= 128 ? 128 : 256;
-  static_assert(kStages >= 2 && 3 * NT <= 256 && NT % 16 == 0, "");
+  static constexpr int kKStages = kStages / 2, kVStages = kStages - kKStages;
+  static constexpr int kSmem = kFixed + kStages * kTile;
+  static constexpr int kNeed = kGroups * 3 * NT;  // columns of tensor memory
+  static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+  static_assert(kStages >= 2 && kNeed <= (kGroups == 1 ? 256 : 512) && NT % 16 == 0, "");
 };
 
+struct GroupBarriers {
+  uint64_t s_full[2], p_full[2], pv_done[2];
+};
 struct TcBarriers {
-  uint64_t k_full[3], v_full[3], s_full[2], p_full[2], pv_done[2], q_full, drained[2];
+  uint64_t k_full[3], v_full[3], q_full, drained[2];
+  GroupBarriers group[2];
   uint32_t tmem, gave_up, fix;
   uint32_t fix_tokens[kBlockWords];  // the block's positions whose values are not finite
 };
@@ -129,23 +138,20 @@ __device__ __forceinline__ float reduce16(float v[16], Op op) {
   return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 16));
 }
 
-template <int NT, int D, bool kTma>
-__global__ void __launch_bounds__(kTcThreads, 2)
+template <int NT, int D, bool kTma, int kGroups>
+__global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 1 ? 2 : 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, AttendArgs a, int32_t row_tiles) {
-  using T = TcShape<NT, D, kTma>;
+  using T = TcShape<NT, D, kGroups>;
+  constexpr int kKeyWarp = 4 * kGroups;
   extern __shared__ uint8_t raw[];
   uint8_t *base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   uint8_t *kring = base, *vring = base + T::kKStages * T::kTile;
-  uint8_t *qs = base + T::kStages * T::kTile;
-  uint8_t *ps = qs + T::kQ;
-  uint32_t *desc = reinterpret_cast<uint32_t *>(ps + T::kPBufs * T::kP);  // [R][kMaskWords]
-  float *nrefs = reinterpret_cast<float *>(desc + PSI_MAX_BLOCK_ROWS * T::kMaskWords);  // [NT]
-  float *facs = nrefs + NT;                                                             // [NT]
-  float *wred = facs + NT;                                                              // [4][NT]
-  int64_t *out_row = reinterpret_cast<int64_t *>(wred + 4 * NT);                        // [NT]
-  TcBarriers *bars = reinterpret_cast<TcBarriers *>(out_row + NT);
-  static_assert(sizeof(TcBarriers) <= 512, "");
+  uint8_t *qs = base + T::kStages * T::kTile;  // [kGroups]
+  uint8_t *ps = qs + kGroups * T::kQ;          // [kGroups][kPBufs]
+  uint8_t *small = ps + kGroups * T::kPBufs * T::kP;
+  TcBarriers *bars = reinterpret_cast<TcBarriers *>(small + kGroups * T::kSmall);
+  static_assert(sizeof(TcBarriers) <= 640, "");
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   if (tid == 0) {
@@ -154,19 +160,21 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       mbar_init(&bars->v_full[s], kTma ? 1 : 32);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&bars->s_full[b], 1);
-      mbar_init(&bars->p_full[b], kSoft);
-      mbar_init(&bars->pv_done[b], 1);
+      for (int g = 0; g < kGroups; ++g) {
+        mbar_init(&bars->group[g].s_full[b], 1);
+        mbar_init(&bars->group[g].p_full[b], kSoft);
+        mbar_init(&bars->group[g].pv_done[b], 1);
+      }
       mbar_init(&bars->drained[b], 1);
     }
-    mbar_init(&bars->q_full, kSoft);
+    mbar_init(&bars->q_full, kGroups * kSoft);
     bars->gave_up = 0;
     bars->fix = 0;
     for (int w = 0; w < kBlockWords; ++w) bars->fix_tokens[w] = 0;
     fence_mbar_init();
   }
-  if (warp == 4) tmem_alloc(&bars->tmem, T::kCols);
-  if (kTma && tid == 5 * 32) {
+  if (warp == kKeyWarp) tmem_alloc(&bars->tmem, T::kCols);
+  if (kTma && tid == (kKeyWarp + 1) * 32) {
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 
   // full ranges come first, the ends of the longest sequences last
   int id = blockIdx.x;
-  const int row0 = id % row_tiles * NT;
+  const int tile0 = id % row_tiles * (NT * kGroups);  // the CTA's first packed row
   id /= row_tiles;
   const int h = id % a.kv_heads;
   id /= a.kv_heads;
@@ -191,17 +199,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   const int begin = split < range.units ? split * range.per : total;
   const int end = total - begin < range.per ? total : begin + range.per;
   const int tiles = (end - begin + kTok - 1) / kTok;  // 0: nothing for this CTA
-  if (tid < NT) {  // where the packed rows go
-    const int pr = row0 + tid;
-    out_row[tid] = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
-  }
   __syncthreads();
   const uint32_t tmem = bars->tmem;
   volatile uint32_t *gave_up = &bars->gave_up;
 
-  if (tiles > 0 && (warp == 4 || warp == 5)) {
-    // ---- loads and products of keys (warp 4) or values (warp 5)
-    const bool keys = warp == 4;
+  if (tiles > 0 && warp >= kKeyWarp) {
+    // ---- loads and products of keys, or of values (the last warp)
+    const bool keys = warp == kKeyWarp;
     const int stages = keys ? T::kKStages : T::kVStages;
     uint8_t *ring = keys ? kring : vring;
     uint64_t *full = keys ? bars->k_full : bars->v_full;
@@ -265,57 +269,81 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const int slot = i % stages, b = i & 1, phase = (i >> 1) & 1;
       const uint32_t at = smem_addr(ring + slot * T::kTile);
       ok = ok && wait_or_give_up(&full[slot], (i / stages) & 1, gave_up);
-      if (keys) {
-        // S^T's buffer is free once the tile before last has its weights
-        if (i >= 2) ok = ok && wait_or_give_up(&bars->p_full[b], ((i - 2) >> 1) & 1, gave_up);
-      } else {
-        ok = ok && wait_or_give_up(&bars->p_full[b], phase, gave_up);
-      }
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      fence_async_shared();
-      tc_fence_after();
-      if (lane == 0) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        GroupBarriers &bar = bars->group[g];
         if (keys) {
-          const uint32_t q = smem_addr(qs);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc_product(tmem + b * NT,
-                       operand(at + k / 4 * (kTok * 128) + k % 4 * 32, 16, 1024, 2),
-                       operand(q + k / 4 * (NT * 128) + k % 4 * 32, 16, 1024, 2), kScores, k > 0);
-          tc_commit(&bars->s_full[b]);
+          // S^T's buffer is free once the tile before last has its weights
+          if (i >= 2) ok = ok && wait_or_give_up(&bar.p_full[b], ((i - 2) >> 1) & 1, gave_up);
         } else {
-          // V^T: 64-element columns a sub-tile apart (the same one twice for
-          // D = 64: the upper half of O^T is not read), 8 positions 1 KB
-          // apart.  P^T: 8 positions 128 bytes apart, 8 rows 2 KB.
-          const uint32_t pt = smem_addr(ps) + i % T::kPBufs * T::kP;
-#pragma unroll
-          for (int k = 0; k < kTok / 16; ++k)
-            tc_product(tmem + 2 * NT, operand(at + k * 2048, D == 128 ? kTok * 128 : 0, 1024, 2),
-                       operand(pt + k * 256, 128, 2048, 0), kValues, i > 0 || k > 0);
-          tc_commit(&bars->pv_done[b]);
+          ok = ok && wait_or_give_up(&bar.p_full[b], phase, gave_up);
         }
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok && lane == 0) {
+          fence_async_shared();
+          tc_fence_after();
+          const uint32_t cols = tmem + g * 3 * NT;
+          if (keys) {
+            const uint32_t q = smem_addr(qs) + g * T::kQ;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc_product(cols + b * NT, operand(at + k / 4 * (kTok * 128) + k % 4 * 32, 16, 1024, 2),
+                         operand(q + k / 4 * (NT * 128) + k % 4 * 32, 16, 1024, 2), kScores, k > 0);
+            tc_commit(&bar.s_full[b]);
+          } else {
+            // V^T: 64-element columns a sub-tile apart (the same one twice
+            // for D = 64: the upper half of O^T is not read), 8 positions
+            // 1 KB apart.  P^T: 8 positions 128 bytes apart, 8 rows 2 KB.
+            const uint32_t pt = smem_addr(ps) + (g * T::kPBufs + i % T::kPBufs) * T::kP;
+#pragma unroll
+            for (int k = 0; k < kTok / 16; ++k)
+              tc_product(cols + 2 * NT, operand(at + k * 2048, D == 128 ? kTok * 128 : 0, 1024, 2),
+                         operand(pt + k * 256, 128, 2048, 0), kValues, i > 0 || k > 0);
+            tc_commit(&bar.pv_done[b]);
+          }
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      if (loaded < tiles) {  // the stage is free once the product that reads it is done
-        ok = wait_or_give_up(keys ? &bars->s_full[b] : &bars->pv_done[b], phase, gave_up);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      if (!ok) break;
+      if (loaded < tiles) {  // the stage is free once the last product that reads it is done
+        GroupBarriers &bar = bars->group[kGroups - 1];
+        ok = wait_or_give_up(keys ? &bar.s_full[b] : &bar.pv_done[b], phase, gave_up);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
         load();
       }
     }
     if (!kTma) copy_wait_all();
     if (*gave_up) {  // let what was issued end before tensor memory is freed
-      if (lane == 0) tc_commit(&bars->drained[warp - 4]);
-      mbar_wait_bounded(&bars->drained[warp - 4], 0);
+      if (lane == 0) tc_commit(&bars->drained[warp - kKeyWarp]);
+      mbar_wait_bounded(&bars->drained[warp - kKeyWarp], 0);
     }
   } else if (tiles > 0) {
     // ---- softmax: one thread per position of the tile
-    const uint32_t lanes = (uint32_t)warp << 21;  // this warp's 32 lanes of tensor memory
+    const int g = warp / 4, st = tid % kSoft;  // group, thread of the group
+    const int sync = 1 + g;                    // the group's barrier
+    GroupBarriers &bar = bars->group[g];
+    uint8_t *mine = small + g * T::kSmall;
+    int64_t *out_at = reinterpret_cast<int64_t *>(mine);              // [NT] the row's result
+    float *nrefs = reinterpret_cast<float *>(out_at + NT);            // [NT]
+    float *facs = nrefs + NT;                                         // [NT]
+    float *wred = facs + NT;                                          // [4][NT]
+    uint32_t *desc = reinterpret_cast<uint32_t *>(wred + 4 * NT);     // [R][kMaskWords]
+    uint8_t *q_own = qs + g * T::kQ, *p_own = ps + g * T::kPBufs * T::kP;
+    const int row0 = tile0 + g * NT;
+    // this warp's 32 lanes of the group's columns of tensor memory
+    const uint32_t own = tmem + ((uint32_t)(warp % 4) << 21) + g * 3 * NT;
+    if (st < NT) {
+      const int pr = row0 + st;
+      const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
+      out_at[st] = (joined ? row * a.splits + split : row) * D;
+    }
     {
       constexpr int kMine = NT * D / 8 / kSoft;
       uint4 x[kMine];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int r = (tid + i * kSoft) / (D / 8), c = (tid + i * kSoft) % (D / 8), pr = row0 + r;
+        const int r = (st + i * kSoft) / (D / 8), c = (st + i * kSoft) % (D / 8), pr = row0 + r;
         x[i] = make_uint4(0, 0, 0, 0);
         if (pr < rows)
           x[i] = *reinterpret_cast<const uint4 *>(
@@ -324,35 +352,35 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int r = (tid + i * kSoft) / (D / 8), c = (tid + i * kSoft) % (D / 8);
-        *reinterpret_cast<uint4 *>(qs + c / 8 * (NT * 128) + r * 128 + ((c % 8) ^ (r % 8)) * 16) =
+        const int r = (st + i * kSoft) / (D / 8), c = (st + i * kSoft) % (D / 8);
+        *reinterpret_cast<uint4 *>(q_own + c / 8 * (NT * 128) + r * 128 + ((c % 8) ^ (r % 8)) * 16) =
             x[i];
       }
     }
     fence_async_shared();
     mbar_arrive(&bars->q_full);
     // which rows see which of the block's positions; which rows belong to it
-    for (int i = tid; i < a.R * T::kMaskWords; i += kSoft) desc[i] = 0;
-    for (int j = tid; j < NT; j += kSoft) nrefs[j] = -kUnset;
+    for (int i = st; i < a.R * T::kMaskWords; i += kSoft) desc[i] = 0;
+    for (int j = st; j < NT; j += kSoft) nrefs[j] = -kUnset;
     bool bad_page = false;
-    for (int i = begin / a.g.page_size + tid; i <= (end - 1) / a.g.page_size; i += kSoft)
+    for (int i = begin / a.g.page_size + st; i <= (end - 1) / a.g.page_size; i += kSoft)
       bad_page |= table[i] < 0 || table[i] >= a.g.num_pages;
-    if (a.dev_status && (bad_page || (want > cap && tid == 0)))
+    if (a.dev_status && (bad_page || (want > cap && st == 0)))
       atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
-    bad_page = named_or(1, kSoft, bad_page);
+    bad_page = named_or(sync, kSoft, bad_page);
     if (!parents) {  // a chain: position x is seen by the rows from x * G on
-      for (int i = tid; i < a.R * T::kMaskWords; i += kSoft) {
+      for (int i = st; i < a.R * T::kMaskWords; i += kSoft) {
         const int w = i % T::kMaskWords, first = i / T::kMaskWords * G - row0 - w * 32;
         const int last = rows - row0 - w * 32;  // rows past the block see nothing
         const uint32_t from = first <= 0 ? 0xFFFFFFFFu : first >= 32 ? 0u : 0xFFFFFFFFu << first;
         const uint32_t to = last >= 32 ? 0xFFFFFFFFu : last <= 0 ? 0u : (1u << last) - 1u;
         desc[i] = from & to;
       }
-    } else if (tid < NT && row0 + tid < rows) {
-      int r = (row0 + tid) / G;
+    } else if (st < NT && row0 + st < rows) {
+      int r = (row0 + st) / G;
       if (row_depth(parents, r) >= 0) {
         for (;;) {
-          atomicOr(desc + r * T::kMaskWords + tid / 32, 1u << (tid % 32));
+          atomicOr(desc + r * T::kMaskWords + st / 32, 1u << (st % 32));
           if (r == 0) break;
           r = parents[r - 1] + 1;
         }
@@ -360,13 +388,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         atomicOr(a.dev_status, PSI_DEV_BAD_PARENT);
       }
     }
-    named_sync(1, kSoft);
+    named_sync(sync, kSoft);
 
     float l[NT];  // sums of this thread's positions
 #pragma unroll
     for (int j = 0; j < NT; ++j) l[j] = 0.f;
     for (int i = 0; i < tiles; ++i) {
-      const int t = begin + i * kTok + tid;
+      const int t = begin + i * kTok + st;
       // rows that see this thread's position
       uint32_t seen[T::kMaskWords];
       const bool masked = begin + (i + 1) * kTok > (len < end ? len : end) || bad_page;
@@ -380,20 +408,20 @@ __global__ void __launch_bounds__(kTcThreads, 2)
           seen[w] = !there ? 0u : t < len ? 0xFFFFFFFFu : desc[(t - len) * T::kMaskWords + w];
       }
       // (a wait that gives up leaves garbage behind and the status says so)
-      wait_or_give_up(&bars->s_full[i & 1], (i >> 1) & 1, gave_up);
+      wait_or_give_up(&bar.s_full[i & 1], (i >> 1) & 1, gave_up);
       __syncwarp();
       tc_fence_after();
-      const uint32_t st = tmem + lanes + (i & 1) * NT;
+      const uint32_t scores = own + (i & 1) * NT;
       uint32_t packed[NT / 2];
       const auto weigh_tile = [&](auto mask, auto again) {
         float2 all = make_float2(0.f, 0.f);
         float s[2][16];
-        tmem_ld16(st, s[0]);
+        tmem_ld16(scores, s[0]);
 #pragma unroll
         for (int c = 0; c < NT; c += 16) {
           const int b = c / 16 % 2;
           tmem_wait_ld16(s[b]);
-          if (c + 16 < NT) tmem_ld16(st + c + 16, s[1 - b]);
+          if (c + 16 < NT) tmem_ld16(scores + c + 16, s[1 - b]);
           weigh<mask.value, again.value>(s[b], a.scale2, nrefs + c, facs + c,
                                          seen[c / 32] >> (c % 32), l + c, all, packed + c / 2);
         }
@@ -401,18 +429,37 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       };
       using std::false_type;
       using std::true_type;
-      // the first tile sets the references; later ones seldom raise them
-      bool raise = i == 0;
+      // Any score of a row will do for its first reference: that of the first
+      // position where every row sees it, else the tile's maxima.
+      bool raise = i == 0 && masked;
+      if (i == 0 && !masked) {
+        if (warp % 4 == 0) {
+#pragma unroll 1
+          for (int c = 0; c < NT; c += 16) {
+            float s[16];
+            tmem_ld16(scores + c, s);
+            tmem_wait_ld16(s);
+            if (lane == 0) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float x = s[j] * a.scale2;
+                nrefs[c + j] = fabsf(x) < -kUnset ? -x : -kUnset;
+              }
+            }
+          }
+        }
+        named_sync(sync, kSoft);
+      }
       if (!raise) {
         const float all = masked ? weigh_tile(true_type{}, false_type{})
                                  : weigh_tile(false_type{}, false_type{});
-        raise = named_or(1, kSoft, !(all <= kFar));
+        raise = named_or(sync, kSoft, !(all <= kFar));
       }
       if (raise) {
 #pragma unroll 1
         for (int c = 0; c < NT; c += 16) {
           float s[16];
-          tmem_ld16(st + c, s);
+          tmem_ld16(scores + c, s);
           tmem_wait_ld16(s);
           constexpr int kLast = T::kMaskWords - 1;
           const uint32_t word = c < 32 ? seen[0] : c < 64 ? seen[kLast < 1 ? kLast : 1] : seen[kLast];
@@ -420,29 +467,29 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
           for (int j = 0; j < 16; ++j) s[j] = (sees >> j) & 1u ? s[j] * a.scale2 : kMinusInf;
           const float m = reduce16(s, [](float x, float y) { return fmaxf(x, y); });
-          if (lane < 16) wred[warp * NT + c + lane] = m;
+          if (lane < 16) wred[warp % 4 * NT + c + lane] = m;
         }
-        named_sync(1, kSoft);
-        if (tid < NT) {
-          const float m = fmaxf(fmaxf(wred[tid], wred[NT + tid]),
-                                fmaxf(wred[2 * NT + tid], wred[3 * NT + tid]));
+        named_sync(sync, kSoft);
+        if (st < NT) {
+          const float m = fmaxf(fmaxf(wred[st], wred[NT + st]),
+                                fmaxf(wred[2 * NT + st], wred[3 * NT + st]));
           // (each row by its own scores: what other rows see does not touch its bits)
-          const float old = -nrefs[tid], now = m > old + kHeadroom ? m : old;
-          facs[tid] = now == old && i > 0 ? 1.f : fast_exp2(old - now);
-          nrefs[tid] = -now;
+          const float old = -nrefs[st], now = m > old + kHeadroom ? m : old;
+          facs[st] = now == old && i > 0 ? 1.f : fast_exp2(old - now);
+          nrefs[st] = -now;
         }
-        if (i > 0) wait_or_give_up(&bars->pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
-        named_sync(1, kSoft);
+        if (i > 0) wait_or_give_up(&bar.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
+        named_sync(sync, kSoft);
         tc_fence_after();
         if (i > 0) {
 #pragma unroll 1
           for (int c = 0; c < NT; c += 16) {
             float o[16];
-            tmem_ld16(tmem + lanes + 2 * NT + c, o);
+            tmem_ld16(own + 2 * NT + c, o);
             tmem_wait_ld16(o);
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] *= facs[c + j];
-            tmem_st16(tmem + lanes + 2 * NT + c, o);
+            tmem_st16(own + 2 * NT + c, o);
           }
           tmem_wait_st();
         }
@@ -451,10 +498,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       // the buffer of P^T is free once its last product is done
       if (i >= T::kPBufs) {
         const int x = i - T::kPBufs;
-        wait_or_give_up(&bars->pv_done[x & 1], (x >> 1) & 1, gave_up);
+        wait_or_give_up(&bar.pv_done[x & 1], (x >> 1) & 1, gave_up);
         __syncwarp();
       }
-      uint8_t *pt = ps + i % T::kPBufs * T::kP + tid / 8 * 128 + tid % 8 * 16;
+      uint8_t *pt = p_own + i % T::kPBufs * T::kP + st / 8 * 128 + st % 8 * 16;
 #pragma unroll
       for (int c = 0; c < NT / 2; c += 4)
         *reinterpret_cast<uint4 *>(pt + c / 4 * 2048) =
@@ -463,7 +510,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         // what lies here is no value of the sequence: 0 * NaN is not 0
         const int slot = i % T::kVStages;
         wait_or_give_up(&bars->v_full[slot], (i / T::kVStages) & 1, gave_up);
-        uint8_t *v = vring + slot * T::kTile + tid * 128;
+        uint8_t *v = vring + slot * T::kTile + st * 128;
         for (int c = 0; c < D / 8; ++c)
           *reinterpret_cast<uint4 *>(v + c / 8 * (kTok * 128) + c % 8 * 16) = make_uint4(0, 0, 0, 0);
       }
@@ -472,11 +519,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         // is taken out here if it is not finite, and added at the end
         const int slot = i % T::kVStages;
         wait_or_give_up(&bars->v_full[slot], (i / T::kVStages) & 1, gave_up);
-        uint8_t *v = vring + slot * T::kTile + tid * 128;
+        uint8_t *v = vring + slot * T::kTile + st * 128;
         bool fix = false;
         for (int c = 0; c < D / 8; ++c) {
           uint16_t *at = reinterpret_cast<uint16_t *>(v + c / 8 * (kTok * 128) +
-                                                      ((c % 8) ^ (tid % 8)) * 16);
+                                                      ((c % 8) ^ (st % 8)) * 16);
           if (!vec_maybe_nonfinite<uint16_t>(*reinterpret_cast<const uint4 *>(at))) continue;
           for (int k = 0; k < 8; ++k)
             if (not_finite(at[k])) {
@@ -491,41 +538,41 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       }
       tc_fence_before();
       fence_async_shared();
-      mbar_arrive(&bars->p_full[i & 1]);
+      mbar_arrive(&bar.p_full[i & 1]);
     }
 
     // ---- results
-    wait_or_give_up(&bars->pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, gave_up);
+    wait_or_give_up(&bar.pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, gave_up);
     __syncwarp();
     tc_fence_after();
 #pragma unroll
     for (int c = 0; c < NT; c += 16) {  // add up the lanes
       const float sum = reduce16(l + c, [](float x, float y) { return x + y; });
-      if (lane < 16) wred[warp * NT + c + lane] = sum;
+      if (lane < 16) wred[warp % 4 * NT + c + lane] = sum;
     }
-    named_sync(1, kSoft);
-    if (tid < NT) {
+    named_sync(sync, kSoft);
+    if (st < NT) {
       // the root's bits: the rows that belong to the block
-      const bool live = row0 + tid < rows && ((desc[tid / 32] >> (tid % 32)) & 1u);
+      const bool live = row0 + st < rows && ((desc[st / 32] >> (st % 32)) & 1u);
       const float s = !live ? 0.f
-                            : wred[tid] + wred[NT + tid] + wred[2 * NT + tid] + wred[3 * NT + tid];
-      facs[tid] = s == 0.f ? 0.f : 1.f / s;
-      if (row0 + tid < rows) {
+                            : wred[st] + wred[NT + st] + wred[2 * NT + st] + wred[3 * NT + st];
+      facs[st] = s == 0.f ? 0.f : 1.f / s;
+      if (row0 + st < rows) {
+        const int64_t at = out_at[st] / D;
         if (joined)
-          a.part_ml[out_row[tid] * a.splits + split] =
-              make_float2(s == 0.f ? kMinusInf : -nrefs[tid], s);
+          a.part_ml[at] = make_float2(s == 0.f ? kMinusInf : -nrefs[st], s);
         else if (a.out_lse)
-          a.out_lse[out_row[tid]] = s == 0.f ? kMinusInf : -nrefs[tid] * kLn2 + logf(s);
+          a.out_lse[at] = s == 0.f ? kMinusInf : -nrefs[st] * kLn2 + logf(s);
       }
     }
-    named_sync(1, kSoft);
-    const int d = tid;  // O^T: one thread per element of the head
+    named_sync(sync, kSoft);
+    const int d = st;  // O^T: one thread per element of the head
     const bool fix = bars->fix;
-    uint16_t *staged = reinterpret_cast<uint16_t *>(qs);  // (Q has been read)
+    uint16_t *staged = reinterpret_cast<uint16_t *>(q_own);  // (Q has been read)
 #pragma unroll 1
     for (int c = 0; c < NT && row0 + c < rows; c += 16) {
       float o[16];
-      tmem_ld16(tmem + lanes + 2 * NT + c, o);
+      tmem_ld16(own + 2 * NT + c, o);
       tmem_wait_ld16(o);
       if (d >= D) continue;
       if (fix) {
@@ -555,25 +602,25 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       } else {
         int64_t at[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) at[j] = out_row[c + j];
+        for (int j = 0; j < 16; ++j) at[j] = out_at[c + j] + d;
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (row0 + c + j < rows) a.part_o[(at[j] * a.splits + split) * D + d] = o[j];
+          if (row0 + c + j < rows) a.part_o[at[j]] = o[j];
       }
     }
     if (!joined) {
-      named_sync(1, kSoft);
-      for (int i = tid; i < NT * D / 8; i += kSoft) {
+      named_sync(sync, kSoft);
+      for (int i = st; i < NT * D / 8; i += kSoft) {
         const int j = i / (D / 8), c = i % (D / 8) * 8;
         if (row0 + j < rows)
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out_o) + out_row[j] * D + c) =
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out_o) + out_at[j] + c) =
               *reinterpret_cast<const uint4 *>(staged + j * D + c);
       }
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kKeyWarp) {
     tc_fence_after();
     tmem_free(tmem, T::kCols);
   }
@@ -612,29 +659,36 @@ bool pool_map(CUtensorMap *map, const AttendArgs &a, const void *pool) {
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, int D, bool kTma>
-cudaError_t launch_shape(const AttendArgs &a, int32_t row_tiles, int64_t ctas, cudaStream_t stream) {
-  using T = TcShape<NT, D, kTma>;
+template <int NT, int D, bool kTma, int kGroups>
+cudaError_t launch_shape(const AttendArgs &a, const AttendPlan &p, cudaStream_t stream) {
+  using T = TcShape<NT, D, kGroups>;
   static DeviceOnce once;
   const cudaError_t e = once([] {
-    return cudaFuncSetAttribute(attend_tc_kernel<NT, D, kTma>,
+    return cudaFuncSetAttribute(attend_tc_kernel<NT, D, kTma, kGroups>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap = {}, vmap = {};
   if (kTma && (!pool_map(&kmap, a, a.k) || !pool_map(&vmap, a, a.v))) return cudaErrorInvalidValue;
-  return launch_pdl(attend_tc_kernel<NT, D, kTma>, dim3((unsigned)ctas), dim3(kTcThreads),
-                    T::kSmem, stream, kmap, vmap, a, row_tiles);
+  return launch_pdl(attend_tc_kernel<NT, D, kTma, kGroups>, dim3((unsigned)p.ctas),
+                    dim3(T::kThreads), T::kSmem, stream, kmap, vmap, a, p.row_tiles);
 }
 
 template <int D, bool kTma>
 cudaError_t launch_dim(const AttendArgs &a, const AttendPlan &p, cudaStream_t stream) {
-  switch (p.rows) {
-    case 16: return launch_shape<16, D, kTma>(a, p.row_tiles, p.ctas, stream);
-    case 32: return launch_shape<32, D, kTma>(a, p.row_tiles, p.ctas, stream);
-    case 48: return launch_shape<48, D, kTma>(a, p.row_tiles, p.ctas, stream);
-    case 64: return launch_shape<64, D, kTma>(a, p.row_tiles, p.ctas, stream);
-    default: return launch_shape<80, D, kTma>(a, p.row_tiles, p.ctas, stream);
+  if (p.groups == 1) {
+    switch (p.rows) {
+      case 16: return launch_shape<16, D, kTma, 1>(a, p, stream);
+      case 32: return launch_shape<32, D, kTma, 1>(a, p, stream);
+      case 48: return launch_shape<48, D, kTma, 1>(a, p, stream);
+      case 64: return launch_shape<64, D, kTma, 1>(a, p, stream);
+      default: return launch_shape<80, D, kTma, 1>(a, p, stream);
+    }
+  }
+  switch (p.rows / 2) {
+    case 48: return launch_shape<48, D, kTma, 2>(a, p, stream);
+    case 64: return launch_shape<64, D, kTma, 2>(a, p, stream);
+    default: return launch_shape<80, D, kTma, 2>(a, p, stream);
   }
 }
 
@@ -644,10 +698,13 @@ bool attend_tc_fits(psi_dtype dtype, int32_t D) {
   return dtype == PSI_DTYPE_BF16 && (D == 64 || D == 128);
 }
 
-// Packed rows per CTA: as few tiles of at most 80 as hold them, evenly filled.
-int attend_tc_rows(int rows) {
-  const int tiles = (rows + 79) / 80;
-  return ((rows + tiles - 1) / tiles + 15) / 16 * 16;
+// Packed rows per CTA, in one group of up to 80 or two: as few CTAs as hold
+// them, evenly filled.
+void attend_tc_rows(int rows, AttendPlan *p) {
+  p->groups = rows <= 80 ? 1 : 2;
+  const int tiles = (rows + 159) / 160 * p->groups;
+  const int each = ((rows + tiles - 1) / tiles + 15) / 16 * 16;
+  p->rows = p->groups * each;
 }
 
 cudaError_t launch_attend_tc(AttendArgs a, const AttendPlan &plan, cudaStream_t stream) {

@@ -30,6 +30,7 @@ struct AttendArgs {
 struct AttendPlan {
   bool tc;        // on the tensor cores
   int32_t rows;   // packed rows per CTA
+  int32_t groups; // of softmax warps per CTA (tensor cores)
   int32_t splits, least, row_tiles;
   int64_t ctas;
   size_t workspace;
@@ -41,7 +42,7 @@ cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan,
 
 // The tensor-core form (psi_attend_tc.cu).
 bool attend_tc_fits(psi_dtype dtype, int32_t D);
-int attend_tc_rows(int rows);
+void attend_tc_rows(int rows, AttendPlan *p);
 cudaError_t launch_attend_tc(AttendArgs a, const AttendPlan &plan, cudaStream_t stream);
 
 struct AppendArgs {
