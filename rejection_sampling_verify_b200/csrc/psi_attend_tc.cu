@@ -22,9 +22,9 @@
 // lane per box); other page sizes gather the rows' 16-byte chunks with
 // asynchronous copies.
 //
-// Warps: four of softmax for each group of NT rows; one that loads keys and
-// issues the products K Q^T; one that loads values and issues V^T P^T.  Keys
-// and values have stages of their own, so that the next keys load while the
+// Warps: four of softmax for each group of NT rows; one each that loads keys,
+// loads values, issues the products K Q^T and issues V^T P^T.  Keys and
+// values have stages of their own, so that the next keys load while the
 // weights of this tile are at work.  Up to 80 packed rows make one group, two
 // CTAs to an SM; more make CTAs of two groups, one to an SM, whose products
 // share the tiles of keys and values (twice the work per loaded tile).
@@ -51,7 +51,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 
 template <int NT, int D, int kGroups>
 struct TcShape {
-  static constexpr int kThreads = kGroups * kSoft + 64;
+  static constexpr int kThreads = kGroups * kSoft + 128;
   static constexpr int kTile = kTok * D * 2;  // bytes of keys or values per stage
   static constexpr int kQ = NT * D * 2;       // per group, as what follows
   static constexpr int kP = NT * kTok * 2;
@@ -64,6 +64,9 @@ struct TcShape {
   static constexpr int kStages = kRoom < 6 ? kRoom : 6;
   static constexpr int kKStages = kStages / 2, kVStages = kStages - kKStages;
   static constexpr int kSmem = kFixed + kStages * kTile;
+  // registers a thread: the launch gives every warp 128 (168 with two groups);
+  // softmax takes what the others leave
+  static constexpr int kSoftRegs = kGroups == 1 ? 168 : 200, kLoadRegs = kGroups == 1 ? 88 : 104;
   static constexpr int kNeed = kGroups * 3 * NT;  // columns of tensor memory
   static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
   static_assert(kStages >= 2 && kNeed <= (kGroups == 1 ? 256 : 512) && NT % 16 == 0, "");
@@ -73,7 +76,7 @@ struct GroupBarriers {
   uint64_t s_full[2], p_full[2], pv_done[2];
 };
 struct TcBarriers {
-  uint64_t k_full[3], v_full[3], q_full, drained[2];
+  uint64_t k_full[3], v_full[3], k_free[3], v_free[3], q_full, drained[2];
   GroupBarriers group[2];
   uint32_t tmem, gave_up, fix;
   uint32_t fix_tokens[kBlockWords];  // the block's positions whose values are not finite
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     attend_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, AttendArgs a, int32_t row_tiles) {
   using T = TcShape<NT, D, kGroups>;
-  constexpr int kKeyWarp = 4 * kGroups;
+  constexpr int kLoadWarp = 4 * kGroups;  // loads keys; then: loads values, K Q^T, V^T P^T
   extern __shared__ uint8_t raw[];
   uint8_t *base = raw + (1024 - (smem_addr(raw) & 1023)) % 1024;
   uint8_t *kring = base, *vring = base + T::kKStages * T::kTile;
@@ -158,6 +161,8 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     for (int s = 0; s < 3; ++s) {
       mbar_init(&bars->k_full[s], kTma ? 1 : 32);
       mbar_init(&bars->v_full[s], kTma ? 1 : 32);
+      mbar_init(&bars->k_free[s], 1);
+      mbar_init(&bars->v_free[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       for (int g = 0; g < kGroups; ++g) {
@@ -173,8 +178,8 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     for (int w = 0; w < kBlockWords; ++w) bars->fix_tokens[w] = 0;
     fence_mbar_init();
   }
-  if (warp == kKeyWarp) tmem_alloc(&bars->tmem, T::kCols);
-  if (kTma && tid == (kKeyWarp + 1) * 32) {
+  if (warp == kLoadWarp) tmem_alloc(&bars->tmem, T::kCols);
+  if (kTma && tid == (kLoadWarp + 1) * 32) {
     prefetch_map(&kmap);
     prefetch_map(&vmap);
   }
@@ -203,83 +208,92 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   const uint32_t tmem = bars->tmem;
   volatile uint32_t *gave_up = &bars->gave_up;
 
-  if (tiles > 0 && warp >= kKeyWarp) {
-    // ---- loads and products of keys, or of values (the last warp)
-    const bool keys = warp == kKeyWarp;
+  if (tiles > 0 && warp >= kLoadWarp) {
+    shrink_registers<T::kLoadRegs>();
+    const bool keys = (warp - kLoadWarp) % 2 == 0;
     const int stages = keys ? T::kKStages : T::kVStages;
     uint8_t *ring = keys ? kring : vring;
-    uint64_t *full = keys ? bars->k_full : bars->v_full;
-    // One box (TMA) or one position of each 32 (copies) is a lane's to find:
-    // looked up one tile ahead.
-    const int boxes = kTma ? kTok / a.box : 1, in_tile = lane % boxes * a.box, sub = lane / boxes;
-    int page = -1;
-    int64_t offs[4];
-    const auto look_up = [&](int i) {
-      if constexpr (kTma) {
-        const int t = begin + i * kTok + in_tile;
-        page = sub < D / 64 && t < end ? page_of(a.g, table, t) : -1;
-      } else {
+    uint64_t *full = keys ? bars->k_full : bars->v_full, *free = keys ? bars->k_free : bars->v_free;
+    if (warp < kLoadWarp + 2) {
+      // ---- loads.  A lane finds one box (TMA) or four positions (copies) of
+      // a tile; the pages are read one tile ahead, and looked at when needed.
+      constexpr int kFind = kTma ? 1 : 4;
+      const int boxes = kTma ? kTok / a.box : 1, in_tile = kTma ? lane % boxes * a.box : lane;
+      const int sub = kTma ? lane / boxes : 0;
+      int32_t found[kFind];
+      const auto look_up = [&](int i) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int t = begin + i * kTok + 32 * x + lane;
-          offs[x] = t < end ? slot_offset(a.g, table, t) : -1;
+        for (int x = 0; x < kFind; ++x) {
+          const int t = begin + i * kTok + 32 * x + in_tile;
+          found[x] = sub < D / 64 && t < end ? table[t / a.g.page_size] : -1;
         }
-      }
-    };
-    int loaded = 0;
-    const auto load = [&]() {
-      const int slot = loaded % stages;
-      const uint32_t dst = smem_addr(ring + slot * T::kTile);
-      if constexpr (kTma) {
-        // boxes lie inside a page: tiles start at multiples of 128
-        // positions, and a box divides the page size
-        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * a.box * 128;
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-        __syncwarp();
-        if (page >= 0)
-          tensor_load(dst + sub * (kTok * 128) + in_tile * 128, keys ? &kmap : &vmap, sub * 64,
-                      (begin + loaded * kTok + in_tile) % a.g.page_size, page, h, &full[slot]);
-      } else {
-        // rows' 16-byte chunks, swizzled by the row as the operands expect
-        constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
-        const int chunk = lane % kLanesPerRow;
-        const uint16_t *pool = static_cast<const uint16_t *>(keys ? a.k : a.v) +
-                               (int64_t)h * a.g.head_stride + chunk * 8;
-        const uint32_t to = dst + chunk / 8 * (kTok * 128);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll 4
-          for (int s = 0; s < 32; s += kRowsPerStep) {
-            const int from = s + lane / kLanesPerRow, row = 32 * x + from;
-            const int64_t off = __shfl_sync(0xFFFFFFFFu, offs[x], from);
-            copy16(to + row * 128 + ((chunk % 8) ^ (row % 8)) * 16, pool + (off < 0 ? 0 : off),
-                   off >= 0);
-          }
-        copy_arrive(&full[slot]);
-      }
-      if (++loaded < tiles) look_up(loaded);
-    };
-    look_up(0);
-    while (loaded < stages && loaded < tiles) load();
-
-    constexpr uint32_t kScores = product_shape(NT, false, false);
-    constexpr uint32_t kValues = product_shape(NT, true, true);
-    bool ok = !keys || wait_or_give_up(&bars->q_full, 0, gave_up);
-    for (int i = 0; i < tiles; ++i) {
-      const int slot = i % stages, b = i & 1, phase = (i >> 1) & 1;
-      const uint32_t at = smem_addr(ring + slot * T::kTile);
-      ok = ok && wait_or_give_up(&full[slot], (i / stages) & 1, gave_up);
-#pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        GroupBarriers &bar = bars->group[g];
-        if (keys) {
-          // S^T's buffer is free once the tile before last has its weights
-          if (i >= 2) ok = ok && wait_or_give_up(&bar.p_full[b], ((i - 2) >> 1) & 1, gave_up);
+      };
+      look_up(0);
+      for (int i = 0; i < tiles; ++i) {
+        const int slot = i % stages;
+        const uint32_t dst = smem_addr(ring + slot * T::kTile);
+        // the stage is free once the products that read it are done
+        bool ok = i < stages || wait_or_give_up(&free[slot], (i / stages - 1) & 1, gave_up);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        if constexpr (kTma) {
+          // boxes lie inside a page: tiles start at multiples of 128
+          // positions, and a box divides the page size
+          const int page = found[0] < a.g.num_pages ? found[0] : -1;
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * a.box * 128;
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+          __syncwarp();
+          if (page >= 0)
+            tensor_load(dst + sub * (kTok * 128) + in_tile * 128, keys ? &kmap : &vmap, sub * 64,
+                        (begin + i * kTok + in_tile) % a.g.page_size, page, h, &full[slot]);
+          if (i + 1 < tiles) look_up(i + 1);
         } else {
-          ok = ok && wait_or_give_up(&bar.p_full[b], phase, gave_up);
+          // rows' 16-byte chunks, swizzled by the row as the operands expect
+          constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
+          const int chunk = lane % kLanesPerRow;
+          const uint16_t *pool = static_cast<const uint16_t *>(keys ? a.k : a.v) +
+                                 (int64_t)h * a.g.head_stride + chunk * 8;
+          const uint32_t to = dst + chunk / 8 * (kTok * 128);
+          int64_t offs[kFind];
+#pragma unroll
+          for (int x = 0; x < kFind; ++x) {
+            const int t = begin + i * kTok + 32 * x + lane;
+            offs[x] = found[x] < 0 || found[x] >= a.g.num_pages
+                          ? -1
+                          : found[x] * a.g.page_stride + (t % a.g.page_size) * a.g.slot_stride;
+          }
+          if (i + 1 < tiles) look_up(i + 1);
+#pragma unroll
+          for (int x = 0; x < kFind; ++x)
+#pragma unroll 4
+            for (int s = 0; s < 32; s += kRowsPerStep) {
+              const int from = s + lane / kLanesPerRow, row = 32 * x + from;
+              const int64_t off = __shfl_sync(0xFFFFFFFFu, offs[x], from);
+              copy16(to + row * 128 + ((chunk % 8) ^ (row % 8)) * 16, pool + (off < 0 ? 0 : off),
+                     off >= 0);
+            }
+          copy_arrive(&full[slot]);
         }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok && lane == 0) {
+      }
+      if (!kTma) copy_wait_all();
+    } else if (lane == 0) {
+      // ---- products, issued by one lane
+      constexpr uint32_t kScores = product_shape(NT, false, false);
+      constexpr uint32_t kValues = product_shape(NT, true, true);
+      bool ok = !keys || wait_or_give_up(&bars->q_full, 0, gave_up);
+      for (int i = 0; ok && i < tiles; ++i) {
+        const int slot = i % stages, b = i & 1, phase = (i >> 1) & 1;
+        const uint32_t at = smem_addr(ring + slot * T::kTile);
+        ok = wait_or_give_up(&full[slot], (i / stages) & 1, gave_up);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          GroupBarriers &bar = bars->group[g];
+          if (keys) {
+            // S^T's buffer is free once the tile before last has its weights
+            if (i >= 2) ok = ok && wait_or_give_up(&bar.p_full[b], ((i - 2) >> 1) & 1, gave_up);
+          } else {
+            ok = ok && wait_or_give_up(&bar.p_full[b], phase, gave_up);
+          }
+          if (!ok) break;
           fence_async_shared();
           tc_fence_after();
           const uint32_t cols = tmem + g * 3 * NT;
@@ -302,24 +316,17 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
             tc_commit(&bar.pv_done[b]);
           }
         }
-        __syncwarp();
+        if (ok) tc_commit(&free[slot]);
       }
-      if (!ok) break;
-      if (loaded < tiles) {  // the stage is free once the last product that reads it is done
-        GroupBarriers &bar = bars->group[kGroups - 1];
-        ok = wait_or_give_up(keys ? &bar.s_full[b] : &bar.pv_done[b], phase, gave_up);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        load();
+      if (!ok) {  // given up: let what was issued end before tensor memory is freed
+        uint64_t *drained = &bars->drained[keys ? 0 : 1];
+        tc_commit(drained);
+        mbar_wait_bounded(drained, 0);
       }
-    }
-    if (!kTma) copy_wait_all();
-    if (*gave_up) {  // let what was issued end before tensor memory is freed
-      if (lane == 0) tc_commit(&bars->drained[warp - kKeyWarp]);
-      mbar_wait_bounded(&bars->drained[warp - kKeyWarp], 0);
     }
   } else if (tiles > 0) {
     // ---- softmax: one thread per position of the tile
+    grow_registers<T::kSoftRegs>();
     const int g = warp / 4, st = tid % kSoft;  // group, thread of the group
     const int sync = 1 + g;                    // the group's barrier
     GroupBarriers &bar = bars->group[g];
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kKeyWarp) {
+  if (warp == kLoadWarp) {
     tc_fence_after();
     tmem_free(tmem, T::kCols);
   }

@@ -146,6 +146,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return *reinterpret_cast<float2 *>(&d);
 }
 
+// ---- registers ---------------------------------------------------------------------
+// A warpgroup's registers per thread from here on (each of its warps calls it).
+template <int kRegs>
+__device__ __forceinline__ void grow_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void shrink_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 // ---- waits --------------------------------------------------------------------------
 // Waits for a phase unless the CTA gave up already; gives up after ~2 s and
 // tells the rest of the CTA.  (The clock is read now and then only: a read
