@@ -228,57 +228,90 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   }
 }
 
-// Adds up the partial results of one output row, in the order of the ranges:
-// one CTA per row, the ranges' elements eight loads at a time.
+// Adds up the partial results of an output row, in an order that depends on
+// their number alone.  kWarps warps per row (1 where rows are many, 4 where
+// they are few and their ranges many): warp w takes ranges w, w + kWarps, ...,
+// four of them in flight at a time; the warps' sums are added in their order.
 constexpr int kJoinThreads = 128;
 constexpr int kMaxSplits = 256;
-template <typename Bits>
+template <typename Bits, int kWarps>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
-  __shared__ float weight[kMaxSplits], top_l[2];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid % 32;
+  constexpr int kRows = kJoinThreads / 32 / kWarps;  // per CTA
+  __shared__ float parts[kWarps > 1 ? kWarps : 1][PSI_MAX_HEAD_DIM];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, w = warp % kWarps;
+  const int64_t row = (int64_t)blockIdx.x * kRows + warp / kWarps;
   pdl_wait();
+  if (row >= (int64_t)a.N * a.R * a.q_heads) return;
   const int len = a.g.lens[row / ((int64_t)a.R * a.q_heads)];
   if (len < 0) return;
   const int64_t cap = table_capacity(a.g), want = (int64_t)len + a.R;
   const int units = deal((int)(want < cap ? want : cap), a.splits, a.least).units;
   if (units == 1) return;  // (the row is written already)
-  if (tid < 32) {
-    const float2 *ml = a.part_ml + row * a.splits;
-    float2 mine[kMaxSplits / 32];
-    float top = kNegInf, l = 0.f;
+  const float2 *ml = a.part_ml + row * a.splits;
+  float top = kNegInf;
+  for (int s = lane; s < units; s += 32)
+    if (ml[s].y != 0.f) top = fmaxf(top, ml[s].x);
+  top = warp_max(top);
+  float l = 0.f;
+  for (int s = lane; s < units; s += 32)
+    if (ml[s].y != 0.f) l = fmaf(fast_exp2(ml[s].x - top), ml[s].y, l);
+  l = warp_sum(l);
+  const float *o = a.part_o + row * a.splits * a.D;
+  float acc[2][4] = {};
+  for (int s0 = w; s0 < units; s0 += 4 * kWarps) {
+    float weight[4];
+    float4 v[4][2];
 #pragma unroll
-    for (int k = 0; k < kMaxSplits / 32; ++k) {
-      mine[k] = k * 32 + lane < units ? ml[k * 32 + lane] : make_float2(kNegInf, 0.f);
-      if (mine[k].y != 0.f) top = fmaxf(top, mine[k].x);
-    }
-    top = warp_max(top);
+    for (int k = 0; k < 4; ++k) {
+      const int s = s0 + k * kWarps;
+      const float2 m = s < units ? ml[s] : make_float2(kNegInf, 0.f);
+      weight[k] = m.y != 0.f ? fast_exp2(m.x - top) : 0.f;
 #pragma unroll
-    for (int k = 0; k < kMaxSplits / 32; ++k) {
-      const float w = mine[k].y != 0.f ? fast_exp2(mine[k].x - top) : 0.f;
-      if (k * 32 < units) weight[k * 32 + lane] = w;
-      if (mine[k].y != 0.f) l = fmaf(w, mine[k].y, l);
+      for (int c = 0; c < 2; ++c) {
+        const int d = lane * 4 + c * 128;
+        v[k][c] = s < units && d < a.D
+                      ? *reinterpret_cast<const float4 *>(o + (int64_t)s * a.D + d)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     }
-    l = warp_sum(l);
-    if (lane == 0) {
-      top_l[0] = l;
-      if (a.out_lse) a.out_lse[row] = l != 0.f ? top * kLn2 + logf(l) : kNegInf;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (weight[k] != 0.f)  // (a range without weight left nothing to read)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          acc[c][0] = fmaf(weight[k], v[k][c].x, acc[c][0]);
+          acc[c][1] = fmaf(weight[k], v[k][c].y, acc[c][1]);
+          acc[c][2] = fmaf(weight[k], v[k][c].z, acc[c][2]);
+          acc[c][3] = fmaf(weight[k], v[k][c].w, acc[c][3]);
+        }
+  }
+  if (kWarps > 1) {
+    for (int k = 0; k < 8; ++k)
+      if (lane * 4 + k / 4 * 128 + k % 4 < a.D)
+        parts[w][lane * 4 + k / 4 * 128 + k % 4] = acc[k / 4][k % 4];
+    __syncthreads();
+    if (w != 0) return;
+    for (int k = 0; k < 8; ++k) {
+      const int d = lane * 4 + k / 4 * 128 + k % 4;
+      for (int x = 1; x < kWarps && d < a.D; ++x) acc[k / 4][k % 4] += parts[x][d];
     }
   }
-  __syncthreads();
-  const float l = top_l[0];
-  for (int d = tid; d < a.D; d += kJoinThreads) {
-    const float *o = a.part_o + row * a.splits * a.D + d;
-    float acc = 0.f;
-    for (int s0 = 0; s0 < units; s0 += 8) {
-      float v[8];
+  if (lane == 0 && a.out_lse) a.out_lse[row] = l != 0.f ? top * kLn2 + logf(l) : kNegInf;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = s0 + k < units ? o[(int64_t)(s0 + k) * a.D] : 0.f;
+  for (int c = 0; c < 2; ++c) {
+    const int d = lane * 4 + c * 128;
+    if (d >= a.D) continue;
+    float r[4];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)  // (a range without weight left nothing to read)
-        if (s0 + k < units && weight[s0 + k] != 0.f) acc = fmaf(weight[s0 + k], v[k], acc);
+    for (int k = 0; k < 4; ++k) r[k] = l != 0.f ? acc[c][k] / l : 0.f;
+    if constexpr (sizeof(Bits) == 2) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(r[0], r[1]), hi = __floats2bfloat162_rn(r[2], r[3]);
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out_o) + row * a.D + d) =
+          make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+    } else {
+      *reinterpret_cast<float4 *>(static_cast<float *>(a.out_o) + row * a.D + d) =
+          make_float4(r[0], r[1], r[2], r[3]);
     }
-    Store<Bits>::put(a.out_o, row * a.D + d, l != 0.f ? acc / l : 0.f);
   }
 }
 
@@ -302,7 +335,10 @@ cudaError_t launch_simt(const AttendArgs &a, const AttendPlan &plan, cudaStream_
 template <typename Bits>
 cudaError_t launch_join(const AttendArgs &a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.N * a.R * a.q_heads;
-  return launch_pdl(join_kernel<Bits>, dim3((unsigned)rows), dim3(kJoinThreads), 0, stream, a);
+  if (rows <= (int64_t)device_sm_count() * 8)  // fewer rows than warps at work
+    return launch_pdl(join_kernel<Bits, 4>, dim3((unsigned)rows), dim3(kJoinThreads), 0, stream, a);
+  return launch_pdl(join_kernel<Bits, 1>, dim3((unsigned)((rows + 3) / 4)), dim3(kJoinThreads), 0,
+                    stream, a);
 }
 
 }  // namespace
