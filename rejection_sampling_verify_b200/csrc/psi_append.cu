@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include "psi_cache.h"
+#include "psi_tcgen05.cuh"
 
 namespace psi {
 namespace {
@@ -69,6 +70,33 @@ __device__ __forceinline__ Raw8<Bits> pack(const float f[8]) {
                           __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
   }
   return r;
+}
+
+// The two partners of eight rotary pairs, from two chunks: the chunks
+// themselves, or (interleaved) their even and odd elements.
+template <typename Bits, bool kInterleaved>
+__device__ __forceinline__ void split(const Raw8<Bits> &x, const Raw8<Bits> &y, float p[8],
+                                      float q[8]) {
+  float f[16];
+  unpack<Bits>(x, true, f);
+  unpack<Bits>(y, true, f + 8);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    p[k] = kInterleaved ? f[2 * k] : f[k];
+    q[k] = kInterleaved ? f[2 * k + 1] : f[8 + k];
+  }
+}
+template <typename Bits, bool kInterleaved>
+__device__ __forceinline__ void merge(const float p[8], const float q[8], Raw8<Bits> &x,
+                                      Raw8<Bits> &y) {
+  float f[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    f[kInterleaved ? 2 * k : k] = p[k];
+    f[kInterleaved ? 2 * k + 1 : 8 + k] = q[k];
+  }
+  x = pack<Bits>(f);
+  y = pack<Bits>(f + 8);
 }
 
 // scale * (cos, sin) of position * inv_freq.  Whole turns are taken off in
@@ -152,27 +180,54 @@ __global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a
   }
 }
 
-// Rotary halves of whole 8-element chunks: one thread per chunk.
+// Heads of whole 16-element pairs of chunks: one thread per pair.
 //
-// What bounds it is the traffic (each head read once and written once), so
-// everything moves in 16-byte vectors, four of them in flight per thread;
-// a head's chunks lie in one aligned group of kWidth lanes, which add up its
-// squares and exchange its rotary partners without shared memory.  kRows rows
-// of the block share a CTA: four when there are rows enough to fill the
-// device, so that the angles (one per thread) and the row lookups are paid
-// once for four rows; one otherwise.
-template <typename Bits, int kWidth, int kRows>
-__global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(AppendArgs a) {
-  constexpr int kWarps = kAppendThreads / 32, kHeads = 32 / kWidth;  // heads per warp
-  constexpr int kAhead = sizeof(Bits) == 2 ? 4 : 2;
+// What bounds it is the traffic (each head is read once and written once) as
+// long as few instructions are spent per element.  So a thread holds both
+// partners of eight rotary pairs, and its factors (weight times cosine and
+// sine) stay in registers for all heads of a row: a pair costs four products
+// on packed floats, and the only exchange is the sum of squares over the
+// kWidth lanes of a head.  Everything moves in 16-byte vectors, the next
+// head's on their way while one is at work.  kRows rows of the block share a
+// CTA: four when there are rows enough to fill the device, one otherwise.
+template <typename Bits, int kWidth, int kRows, bool kInterleaved>
+__global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a) {
+  constexpr int kWarps = kAppendThreads / 32 / kRows;  // per row
+  constexpr int kHeads = 32 / kWidth, kStep = kWarps * kHeads;
+  constexpr int kAhead = 2;
   __shared__ __align__(16) float cs[kRows][PSI_MAX_HEAD_DIM / 2], sn[kRows][PSI_MAX_HEAD_DIM / 2];
   __shared__ int32_t tree[kRows][PSI_MAX_BLOCK_ROWS];
   __shared__ int64_t slot[kRows], position[kRows];
   const int64_t first = (int64_t)blockIdx.x * kRows, rows = (int64_t)a.N * a.R;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int mine = warp / kWarps, w = warp % kWarps;  // the warp's row, its place among the row's
+  const int64_t row = first + mine;
+  const int half = a.rotary_dim / 2, pair = lane % kWidth * 8;
+  // this lane's two chunks of a head: rotary partners, or neighbours
+  int c1 = 2 * pair, c2 = c1 + 8;
+  if (!kInterleaved) {
+    c1 = pair < half ? pair : a.rotary_dim + (pair - half) * 2;
+    c2 = pair < half ? pair + half : c1 + 8;
+  }
+  const bool in_head = 2 * pair < a.D;
+  const int h0 = w * kHeads + lane / kWidth;
   pdl_wait();
-  if (warp < kRows) {  // one warp finds a row's place
-    const int64_t row = first + warp;
+
+  struct Item {
+    Raw8<Bits> x, y;
+  };
+  const auto fetch = [&](const void *src, int64_t at, bool there, Item &it) {
+    if (!there) return;
+    it.x = load_raw<Bits>(src, at + c1);
+    it.y = load_raw<Bits>(src, at + c2);
+  };
+  Item ahead[kAhead];
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x)
+    fetch(a.q, row * a.q_row + (h0 + x * kStep) * a.q_head,
+          row < rows && in_head && h0 + x * kStep < a.q_heads, ahead[x]);
+
+  if (w == 0) {  // one warp finds a row's place
     int64_t at = -1, pos = -1;
     if (row < rows) {
       const int n = (int)(row / a.R), r = (int)(row % a.R);
@@ -180,8 +235,8 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(AppendArgs a)
       const int32_t *parents = nullptr;
       if (a.parents) {  // (walked in shared memory: a chain of global loads is slow)
         for (int i = lane; i < r; i += 32)
-          tree[warp][i] = a.parents[(int64_t)n * (a.R - 1) + i];
-        parents = tree[warp];
+          tree[mine][i] = a.parents[(int64_t)n * (a.R - 1) + i];
+        parents = tree[mine];
       }
       __syncwarp();
       if (len >= 0) {
@@ -196,12 +251,11 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(AppendArgs a)
       }
     }
     if (lane == 0) {
-      slot[warp] = at;
-      position[warp] = pos;
+      slot[mine] = at;
+      position[mine] = pos;
     }
   }
   __syncthreads();
-  const int half = a.rotary_dim / 2;
   for (int i = tid; i < kRows * half; i += kAppendThreads) {
     const int r = i / half, k = i % half;
     if (position[r] < 0) continue;
@@ -211,106 +265,125 @@ __global__ void __launch_bounds__(kAppendThreads, 3) append_kernel(AppendArgs a)
   }
   __syncthreads();
 
-  const int c = lane % kWidth * 8;  // this lane's elements of a head
-  const bool in_head = c < a.D;
-  float qw[8], kw[8];
+  if (position[mine] < 0) return;  // (the whole warp)
+
+  float c[8], s[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) qw[k] = kw[k] = 1.f;
-  if (in_head && a.q_weight) load8<Bits>(a.q_weight, c, qw);
-  if (in_head && a.k_weight) load8<Bits>(a.k_weight, c, kw);
-  const int heads = a.q_heads + 2 * a.kv_heads;
-  const int total = kRows * heads, step = kWarps * kHeads;
-  for (int h0 = warp * kHeads + lane / kWidth; h0 - lane / kWidth < total; h0 += kAhead * step) {
-    Raw8<Bits> raw[kAhead];
-    Bits *to[kAhead];
-    bool live[kAhead];
+  for (int k = 0; k < 8; ++k) {
+    const bool turned = pair + k < half;
+    c[k] = turned ? cs[mine][pair + k] : 1.f;
+    s[k] = turned ? sn[mine][pair + k] : 0.f;
+  }
+  // One line of heads: norm, turn and store.
+  const auto line = [&](const void *src, int64_t at, int64_t head_stride, int heads,
+                        const void *weight, Bits *to, int64_t to_stride, bool fetched) {
+    // y1 = x1 w1 c - x2 w2 s, y2 = x2 w2 c + x1 w1 s, all over the root mean square
+    float2 wc1[4], ws2[4], wc2[4], ws1[4];
+    {
+      float w1[8], w2[8];
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int hs = h0 + x * step, r = hs / heads, h = hs % heads;
-      const int64_t row = first + r;
-      live[x] = hs < total && position[hs < total ? r : 0] >= 0 && in_head;
-      if (!live[x]) continue;
-      const void *src;
-      int64_t from;
-      if (h < a.q_heads) {
-        src = a.q;
-        from = row * a.q_row + h * a.q_head;
-        to[x] = static_cast<Bits *>(a.out_q) + (row * a.q_heads + h) * a.D + c;
-      } else {
-        const bool is_v = h >= a.q_heads + a.kv_heads;
-        const int kh = h - a.q_heads - (is_v ? a.kv_heads : 0);
-        src = is_v ? a.v : a.k;
-        from = row * (is_v ? a.v_row : a.k_row) + kh * (is_v ? a.v_head : a.k_head);
-        to[x] = static_cast<Bits *>(is_v ? a.v_pool : a.k_pool) + slot[r] + kh * a.g.head_stride + c;
-        live[x] = slot[r] >= 0;
-        if (!live[x]) continue;
+      for (int k = 0; k < 8; ++k) w1[k] = w2[k] = 1.f;
+      if (in_head && weight) {
+        Item it;
+        fetch(weight, 0, true, it);
+        split<Bits, kInterleaved>(it.x, it.y, w1, w2);
       }
-      raw[x] = load_raw<Bits>(src, from + c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        wc1[k] = make_float2(w1[2 * k] * c[2 * k], w1[2 * k + 1] * c[2 * k + 1]);
+        ws1[k] = make_float2(w1[2 * k] * s[2 * k], w1[2 * k + 1] * s[2 * k + 1]);
+        wc2[k] = make_float2(w2[2 * k] * c[2 * k], w2[2 * k + 1] * c[2 * k + 1]);
+        ws2[k] = make_float2(-w2[2 * k] * s[2 * k], -w2[2 * k + 1] * s[2 * k + 1]);
+      }
     }
+    if (!fetched) {
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int hs = h0 + x * step, r = hs < total ? hs / heads : 0, h = hs % heads;
-      float y[8];
-      unpack<Bits>(raw[x], live[x], y);
-      const bool is_q = h < a.q_heads, is_v = h >= a.q_heads + a.kv_heads;
-      float sum = 0.f;  // (every lane of the warp takes the exchanges)
+      for (int x = 0; x < kAhead; ++x)
+        fetch(src, at + (h0 + x * kStep) * head_stride, in_head && h0 + x * kStep < heads, ahead[x]);
+    }
+    for (int h = h0; h - h0 < heads - w * kHeads; h += kAhead * kStep) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = fmaf(y[k], y[k], sum);
+      for (int x = 0; x < kAhead; ++x) {
+        const int hh = h + x * kStep;
+        const bool there = in_head && hh < heads;
+        float x1[8], x2[8];
 #pragma unroll
-      for (int o = kWidth / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-      const bool norm = is_q ? a.q_weight != nullptr : a.k_weight != nullptr;
-      const float inv = norm ? rsqrtf(sum / a.D + a.eps) : 1.f;
+        for (int k = 0; k < 8; ++k) x1[k] = x2[k] = 0.f;
+        if (there) split<Bits, kInterleaved>(ahead[x].x, ahead[x].y, x1, x2);
+        fetch(src, at + (hh + kAhead * kStep) * head_stride, in_head && hh + kAhead * kStep < heads,
+              ahead[x]);
+        float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] *= inv * (is_q ? qw[k] : kw[k]);
-      if (!a.interleaved) {
-        // elements k and k + half are partners: whole chunks apart
-        const bool second = c >= half;
-        const int mate = (lane & ~(kWidth - 1)) | (((second ? c - half : c + half) / 8) & (kWidth - 1));
-        float z[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) z[k] = __shfl_sync(0xFFFFFFFFu, y[k], mate);
-        if (c < a.rotary_dim) {
-          const float *ct = cs[r] + (second ? c - half : c), *st = sn[r] + (second ? c - half : c);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            y[k] = fmaf(y[k], ct[k], (second ? z[k] : -z[k]) * st[k]);
+        for (int k = 0; k < 8; k += 2) {
+          const float2 u = make_float2(x1[k], x1[k + 1]), v = make_float2(x2[k], x2[k + 1]);
+          sq = fma2(v, v, fma2(u, u, sq));
         }
-      } else if (c < a.rotary_dim) {
-        const float *ct = cs[r] + c / 2, *st = sn[r] + c / 2;
+        float sum = sq.x + sq.y;  // (every lane of the warp takes the exchanges)
+#pragma unroll
+        for (int o = kWidth / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float inv = weight ? rsqrtf(sum / a.D + a.eps) : 1.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float p = y[2 * k], q = y[2 * k + 1];
-          y[2 * k] = fmaf(p, ct[k], -q * st[k]);
-          y[2 * k + 1] = fmaf(q, ct[k], p * st[k]);
+          const float2 u = make_float2(x1[2 * k] * inv, x1[2 * k + 1] * inv);
+          const float2 v = make_float2(x2[2 * k] * inv, x2[2 * k + 1] * inv);
+          const float2 zero = make_float2(0.f, 0.f);
+          const float2 y1 = fma2(u, wc1[k], fma2(v, ws2[k], zero));
+          const float2 y2 = fma2(v, wc2[k], fma2(u, ws1[k], zero));
+          x1[2 * k] = y1.x;
+          x1[2 * k + 1] = y1.y;
+          x2[2 * k] = y2.x;
+          x2[2 * k + 1] = y2.y;
+        }
+        if (there) {
+          Raw8<Bits> y1, y2;
+          merge<Bits, kInterleaved>(x1, x2, y1, y2);
+          store_raw<Bits>(to + hh * to_stride + c1, y1);
+          store_raw<Bits>(to + hh * to_stride + c2, y2);
         }
       }
-      if (!live[x]) continue;
-      if (is_v)
-        store_raw<Bits>(to[x], raw[x]);
-      else
-        store_raw<Bits>(to[x], pack<Bits>(y));
+    }
+  };
+  line(a.q, row * a.q_row, a.q_head, a.q_heads, a.q_weight,
+       static_cast<Bits *>(a.out_q) + row * a.q_heads * a.D, a.D, true);
+  const int64_t place = slot[mine];
+  if (place < 0) return;
+  line(a.k, row * a.k_row, a.k_head, a.kv_heads, a.k_weight,
+       static_cast<Bits *>(a.k_pool) + place, a.g.head_stride, false);
+  // values are stored as they are
+  for (int h = h0; h < a.kv_heads; h += kStep) {
+    Item it;
+    fetch(a.v, row * a.v_row + h * a.v_head, in_head, it);
+    if (in_head) {
+      Bits *to = static_cast<Bits *>(a.v_pool) + place + h * a.g.head_stride;
+      store_raw<Bits>(to + c1, it.x);
+      store_raw<Bits>(to + c2, it.y);
     }
   }
 }
 
-template <typename Bits, int kWidth>
+template <typename Bits, int kWidth, bool kInterleaved>
 cudaError_t launch_chunks(const AppendArgs &a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.N * a.R;
   if (rows >= (int64_t)device_sm_count() * 8)
-    return launch_pdl(append_kernel<Bits, kWidth, 4>, dim3((unsigned)((rows + 3) / 4)),
-                      dim3(kAppendThreads), 0, stream, a);
-  return launch_pdl(append_kernel<Bits, kWidth, 1>, dim3((unsigned)rows), dim3(kAppendThreads), 0,
-                    stream, a);
+    return launch_pdl(append_kernel<Bits, kWidth, 4, kInterleaved>,
+                      dim3((unsigned)((rows + 3) / 4)), dim3(kAppendThreads), 0, stream, a);
+  return launch_pdl(append_kernel<Bits, kWidth, 1, kInterleaved>, dim3((unsigned)rows),
+                    dim3(kAppendThreads), 0, stream, a);
+}
+
+template <typename Bits, bool kInterleaved>
+cudaError_t launch_width(const AppendArgs &a, cudaStream_t stream) {
+  if (a.D <= 64) return launch_chunks<Bits, 4, kInterleaved>(a, stream);
+  if (a.D <= 128) return launch_chunks<Bits, 8, kInterleaved>(a, stream);
+  return launch_chunks<Bits, 16, kInterleaved>(a, stream);
 }
 
 template <typename Bits>
 cudaError_t launch_typed(const AppendArgs &a, cudaStream_t stream) {
-  if (a.rotary_dim % (a.interleaved ? 8 : 16) != 0)
+  if (a.D % 16 != 0 || a.rotary_dim % (a.interleaved ? 8 : 16) != 0)
     return launch_pdl(append_any_kernel<Bits>, dim3((unsigned)((int64_t)a.N * a.R)),
                       dim3(kAppendThreads), 0, stream, a);
-  if (a.D <= 64) return launch_chunks<Bits, 8>(a, stream);
-  if (a.D <= 128) return launch_chunks<Bits, 16>(a, stream);
-  return launch_chunks<Bits, 32>(a, stream);
+  return a.interleaved ? launch_width<Bits, true>(a, stream) : launch_width<Bits, false>(a, stream);
 }
 
 }  // namespace
