@@ -221,11 +221,14 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a)
     it.x = load_raw<Bits>(src, at + c1);
     it.y = load_raw<Bits>(src, at + c2);
   };
-  Item ahead[kAhead];
+  // the first heads of each kind are on their way while the place is found
+  Item ahead[kAhead], key, value;
 #pragma unroll
   for (int x = 0; x < kAhead; ++x)
     fetch(a.q, row * a.q_row + (h0 + x * kStep) * a.q_head,
           row < rows && in_head && h0 + x * kStep < a.q_heads, ahead[x]);
+  fetch(a.k, row * a.k_row + h0 * a.k_head, row < rows && in_head && h0 < a.kv_heads, key);
+  fetch(a.v, row * a.v_row + h0 * a.v_head, row < rows && in_head && h0 < a.kv_heads, value);
 
   if (w == 0) {  // one warp finds a row's place
     int64_t at = -1, pos = -1;
@@ -276,7 +279,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a)
   }
   // One line of heads: norm, turn and store.
   const auto line = [&](const void *src, int64_t at, int64_t head_stride, int heads,
-                        const void *weight, Bits *to, int64_t to_stride, bool fetched) {
+                        const void *weight, Bits *to, int64_t to_stride) {
     // y1 = x1 w1 c - x2 w2 s, y2 = x2 w2 c + x1 w1 s, all over the root mean square
     float2 wc1[4], ws2[4], wc2[4], ws1[4];
     {
@@ -295,11 +298,6 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a)
         wc2[k] = make_float2(w2[2 * k] * c[2 * k], w2[2 * k + 1] * c[2 * k + 1]);
         ws2[k] = make_float2(-w2[2 * k] * s[2 * k], -w2[2 * k + 1] * s[2 * k + 1]);
       }
-    }
-    if (!fetched) {
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x)
-        fetch(src, at + (h0 + x * kStep) * head_stride, in_head && h0 + x * kStep < heads, ahead[x]);
     }
     for (int h = h0; h - h0 < heads - w * kHeads; h += kAhead * kStep) {
 #pragma unroll
@@ -344,20 +342,22 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a)
     }
   };
   line(a.q, row * a.q_row, a.q_head, a.q_heads, a.q_weight,
-       static_cast<Bits *>(a.out_q) + row * a.q_heads * a.D, a.D, true);
+       static_cast<Bits *>(a.out_q) + row * a.q_heads * a.D, a.D);
   const int64_t place = slot[mine];
   if (place < 0) return;
+  ahead[0] = key;
+#pragma unroll
+  for (int x = 1; x < kAhead; ++x)
+    fetch(a.k, row * a.k_row + (h0 + x * kStep) * a.k_head,
+          in_head && h0 + x * kStep < a.kv_heads, ahead[x]);
   line(a.k, row * a.k_row, a.k_head, a.kv_heads, a.k_weight,
-       static_cast<Bits *>(a.k_pool) + place, a.g.head_stride, false);
+       static_cast<Bits *>(a.k_pool) + place, a.g.head_stride);
   // values are stored as they are
-  for (int h = h0; h < a.kv_heads; h += kStep) {
-    Item it;
-    fetch(a.v, row * a.v_row + h * a.v_head, in_head, it);
-    if (in_head) {
-      Bits *to = static_cast<Bits *>(a.v_pool) + place + h * a.g.head_stride;
-      store_raw<Bits>(to + c1, it.x);
-      store_raw<Bits>(to + c2, it.y);
-    }
+  for (int h = h0; in_head && h < a.kv_heads; h += kStep) {
+    Bits *to = static_cast<Bits *>(a.v_pool) + place + h * a.g.head_stride;
+    store_raw<Bits>(to + c1, value.x);
+    store_raw<Bits>(to + c2, value.y);
+    fetch(a.v, row * a.v_row + (h + kStep) * a.v_head, h + kStep < a.kv_heads, value);
   }
 }
 
