@@ -8,7 +8,7 @@
 namespace psi {
 namespace {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
 
 template <typename Bits>
 __device__ __forceinline__ float load1(const void *base, int64_t at) {
@@ -189,9 +189,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a
 // on packed floats, and the only exchange is the sum of squares over the
 // kWidth lanes of a head.  Everything moves in 16-byte vectors, the next
 // head's on their way while one is at work.  kRows rows of the block share a
-// CTA: four when there are rows enough to fill the device, one otherwise.
+// CTA: two when there are rows enough to fill the device, one otherwise (four
+// warps a CTA wait for fewer than eight would: 95 against 99 us for 17,408
+// rows of 32 + 2 x 8 heads of 128).
 template <typename Bits, int kWidth, int kRows, bool kInterleaved>
-__global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendArgs a) {
   constexpr int kWarps = kAppendThreads / 32 / kRows;  // per row
   constexpr int kHeads = 32 / kWidth, kStep = kWarps * kHeads;
   constexpr int kAhead = 2;
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a)
   fetch(a.k, row * a.k_row + h0 * a.k_head, row < rows && in_head && h0 < a.kv_heads, key);
   fetch(a.v, row * a.v_row + h0 * a.v_head, row < rows && in_head && h0 < a.kv_heads, value);
 
+  const double first_freq = tid < kRows * half ? a.inv_freq[tid % half] : 0.0;
   if (w == 0) {  // one warp finds a row's place
     int64_t at = -1, pos = -1;
     if (row < rows) {
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(kAppendThreads, 2) append_kernel(AppendArgs a)
   for (int i = tid; i < kRows * half; i += kAppendThreads) {
     const int r = i / half, k = i % half;
     if (position[r] < 0) continue;
-    const float2 t = turn(position[r], a.inv_freq[k], a.rope_scale);
+    const float2 t = turn(position[r], i == tid ? first_freq : a.inv_freq[k], a.rope_scale);
     cs[r][k] = t.x;
     sn[r][k] = t.y;
   }
@@ -365,8 +368,8 @@ template <typename Bits, int kWidth, bool kInterleaved>
 cudaError_t launch_chunks(const AppendArgs &a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.N * a.R;
   if (rows >= (int64_t)device_sm_count() * 8)
-    return launch_pdl(append_kernel<Bits, kWidth, 4, kInterleaved>,
-                      dim3((unsigned)((rows + 3) / 4)), dim3(kAppendThreads), 0, stream, a);
+    return launch_pdl(append_kernel<Bits, kWidth, 2, kInterleaved>,
+                      dim3((unsigned)((rows + 1) / 2)), dim3(kAppendThreads), 0, stream, a);
   return launch_pdl(append_kernel<Bits, kWidth, 1, kInterleaved>, dim3((unsigned)rows),
                     dim3(kAppendThreads), 0, stream, a);
 }
