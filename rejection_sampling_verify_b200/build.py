@@ -1,9 +1,11 @@
-"""Build the CUDA library ``libpsi_verify.so`` in-tree for sm_100a.
+"""Build the CUDA library ``libpsi_verify.so`` in-tree for sm_100a, and the
+Python extension ``_cache_binding.so``.
 
 ``python -m rejection_sampling_verify_b200.build`` compiles every ``csrc/*.cu``
 with nvcc (``-gencode arch=compute_100a,code=sm_100a``) and links the shared
-library next to this file.  Rebuilds only when a source or header is newer
-than the library.
+library next to this file; ``binding/*.cpp`` is compiled with the host
+compiler against torch's headers.  Rebuilds only when a source or header is
+newer than what it makes.
 """
 from __future__ import annotations
 
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpsi_verify.so")
 BUILD_DIR = os.path.join(HERE, "_build")
+BINDING_SRC = os.path.join(HERE, "binding", "cache_binding.cpp")
+BINDING = os.path.join(HERE, "_cache_binding.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -53,7 +58,32 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def build_binding(force: bool = False) -> str:
+    """The extension module between torch tensors and the cache's entry points."""
+    deps = (BINDING_SRC, os.path.join(INCLUDE, "psi_verify.h"))
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps):
+        return BINDING
+    import torch
+    top = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(top, "include"), os.path.join(top, "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-std=c++17", "-O2", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", sysconfig.get_paths()["include"], "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", INCLUDE, BINDING_SRC, "-o", tmp,
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the binding failed to build:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    build_binding(force)
     if not force and up_to_date():
         return LIB
     nvcc = _nvcc()

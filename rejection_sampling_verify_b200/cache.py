@@ -19,6 +19,7 @@ from __future__ import annotations
 import contextlib
 import ctypes as C
 import math
+import os
 from dataclasses import dataclass
 
 from . import (PSI_OK, PsiError, _check_out, _check_workspace, _device_of, _dtype_code, _nbytes,
@@ -226,6 +227,29 @@ def _block(q, page_table, lens, parents):
     return N, R
 
 
+# The common form of each call (outputs and workspace not given, the current
+# stream) goes through the compiled binding, which checks the tensors as the
+# functions below do; what it does not take comes back here as None.
+_binding = None
+
+
+def _short():
+    global _binding
+    if _binding is None:
+        _torch()  # (the extension's symbols are torch's)
+        lib = load_library()
+        from . import build
+        if not os.path.exists(build.BINDING):
+            build.build_binding()
+        from . import _cache_binding
+        _cache_binding.bind(*(C.cast(getattr(lib, name), C.c_void_p).value for name in (
+            "psi_cache_append", "psi_attend_block_workspace_bytes", "psi_attend_block",
+            "psi_cache_commit", "psi_cache_resize", "psi_cache_fork_workspace_bytes",
+            "psi_cache_fork")))
+        _binding = _cache_binding
+    return _binding
+
+
 # A call's shapes, strides and dtypes decide what it may do: they are checked
 # once, and what was found (the layout, the strides, the workspace's size) is
 # kept under them.
@@ -333,6 +357,13 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight=None, k_w
     inv_freq float64 [rotary_dim / 2] or None; parents int32 [N, R - 1] or
     None (a chain).  ``out.q`` may be ``q`` itself.
     """
+    if out is None and stream is None:
+        r = (_binding or _short()).append(q, k, v, k_pages, v_pages, page_table, lens, q_weight,
+                                          k_weight, eps, inv_freq, interleaved, rope_scale,
+                                          parents)
+        if r is not None:
+            _check(r[0], "psi_cache_append")
+            return AppendResult(r[1], r[2])
     key = ("append", _sig(q), _sig(k), _sig(v), _sig(k_pages), _sig(v_pages), _sig(page_table),
            _sig(lens), _sig(q_weight), _sig(k_weight), _sig(inv_freq), _sig(parents))
     plan = _plans.get(key) or _remember(key, _plan_append(
@@ -390,6 +421,12 @@ def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: flo
     D ** -0.5.  With ``out`` and a large enough ``workspace`` the call only
     launches work on the stream.
     """
+    if out is None and workspace is None and stream is None:
+        r = (_binding or _short()).attend(q, k_pages, v_pages, page_table, lens, parents, scale,
+                                          want_lse)
+        if r is not None:
+            _check(r[0], "psi_attend_block")
+            return AttendResult(r[1], r[2], r[3])
     key = ("attend", _sig(q), _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(lens),
            _sig(parents))
     plan = _plans.get(key) or _remember(key, _plan_attend(q, k_pages, v_pages, page_table, lens,
@@ -441,6 +478,12 @@ def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, strea
     int32 [N] as :func:`verify_tree_greedy` and :func:`verify_tree_sampled`
     return them.  Returns the new lengths (``out.lens`` is not ``lens``).
     """
+    if out is None and stream is None:
+        r = (_binding or _short()).commit(k_pages, v_pages, page_table, lens, path_nodes,
+                                          path_len)
+        if r is not None:
+            _check(r[0], "psi_cache_commit")
+            return CommitResult(r[1], r[2])
     key = ("commit", _sig(k_pages), _sig(v_pages), _sig(page_table), _sig(lens), _sig(path_nodes),
            _sig(path_len))
     plan = _plans.get(key) or _remember(key, _plan_commit(k_pages, v_pages, page_table, lens,
@@ -511,6 +554,12 @@ def cache_resize(pages: PageState, lens, extra: int, page_size: int, stream=None
     """Fit each sequence's pages to lens[n] + extra positions
     (``psi_cache_resize``).  Returns a new state; with ``out.pages = pages``
     the state is changed in place."""
+    if out is None and stream is None:
+        r = (_binding or _short()).resize(pages.table, pages.counts, pages.refs, pages.free,
+                                          pages.n_free, lens, extra, page_size)
+        if r is not None:
+            _check(r[0], "psi_cache_resize")
+            return ResizeResult(PageState(r[1], r[2], r[3], r[4], r[5]), r[6])
     key = ("resize", _state_sig(pages), _sig(lens))
     N, max_pages, P = _plans.get(key) or _remember(key, _plan_resize(pages, lens))
     others = dict(lens=lens, **_named("pages", pages))
@@ -546,6 +595,12 @@ def cache_fork(k_pages, v_pages, pages: PageState, lens, src, dst, workspace=Non
     k_pages, v_pages [L, P, S, H, D]; src, dst int32 [K].  Returns a new
     state and lengths; ``out`` may name the given ones (in place).
     """
+    if out is None and workspace is None and stream is None:
+        r = (_binding or _short()).fork(k_pages, v_pages, pages.table, pages.counts, pages.refs,
+                                        pages.free, pages.n_free, lens, src, dst)
+        if r is not None:
+            _check(r[0], "psi_cache_fork")
+            return ForkResult(PageState(r[1], r[2], r[3], r[4], r[5]), r[6], r[7])
     key = ("fork", _sig(k_pages), _sig(v_pages), _state_sig(pages), _sig(lens), _sig(src),
            _sig(dst))
     plan = _plans.get(key) or _remember(key, _plan_fork(k_pages, v_pages, pages, lens, src, dst))
