@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a
   const int n = (int)(row / a.R), r = (int)(row % a.R);
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_wait();
+  pdl_trigger();
   const int len = a.g.lens[n];
   if (len < 0) return;
   const int depth = row_depth(a.parents ? a.parents + (int64_t)n * (a.R - 1) : nullptr, r);
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendArgs a)
   const bool in_head = 2 * pair < a.D;
   const int h0 = w * kHeads + lane / kWidth;
   pdl_wait();
+  pdl_trigger();
 
   struct Item {
     Raw8<Bits> x, y;

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   const int n = id % a.N, split = id / a.N;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_wait();
+  pdl_trigger();
   const int len = a.g.lens[n];
   if (len < 0) return;  // the sequence is not there
   const int rows = a.R * G;
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, w = warp % kWarps;
   const int64_t row = (int64_t)blockIdx.x * kRows + warp / kWarps;
   pdl_wait();
+  pdl_trigger();
   if (row >= (int64_t)a.N * a.R * a.q_heads) return;
   const int len = a.g.lens[row / ((int64_t)a.R * a.q_heads)];
   if (len < 0) return;
@@ -324,8 +326,11 @@ template <typename Bits>
 cudaError_t launch_simt(const AttendArgs &a, const AttendPlan &plan, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t e = once([] {
-    return cudaFuncSetAttribute(attend_kernel<Bits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)simt_smem(PSI_MAX_HEAD_DIM));
+    const cudaError_t x = prefer_max_shared(attend_kernel<Bits>);
+    return x != cudaSuccess
+               ? x
+               : cudaFuncSetAttribute(attend_kernel<Bits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)simt_smem(PSI_MAX_HEAD_DIM));
   });
   if (e != cudaSuccess) return e;
   return launch_pdl(attend_kernel<Bits>, dim3((unsigned)plan.ctas), dim3(kSimtThreads),
@@ -334,6 +339,12 @@ cudaError_t launch_simt(const AttendArgs &a, const AttendPlan &plan, cudaStream_
 
 template <typename Bits>
 cudaError_t launch_join(const AttendArgs &a, cudaStream_t stream) {
+  static DeviceOnce once;
+  const cudaError_t e = once([] {
+    const cudaError_t x = prefer_max_shared(join_kernel<Bits, 4>);
+    return x != cudaSuccess ? x : prefer_max_shared(join_kernel<Bits, 1>);
+  });
+  if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.N * a.R * a.q_heads;
   if (rows <= (int64_t)device_sm_count() * 8)  // fewer rows than warps at work
     return launch_pdl(join_kernel<Bits, 4>, dim3((unsigned)rows), dim3(kJoinThreads), 0, stream, a);

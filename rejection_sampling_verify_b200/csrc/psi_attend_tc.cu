@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     prefetch_map(&vmap);
   }
   pdl_wait();
+  pdl_trigger();
 
   // full ranges come first, the ends of the longest sequences last
   int id = blockIdx.x;
@@ -671,8 +672,11 @@ cudaError_t launch_shape(const AttendArgs &a, const AttendPlan &p, cudaStream_t 
   using T = TcShape<NT, D, kGroups>;
   static DeviceOnce once;
   const cudaError_t e = once([] {
-    return cudaFuncSetAttribute(attend_tc_kernel<NT, D, kTma, kGroups>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+    const cudaError_t x = prefer_max_shared(attend_tc_kernel<NT, D, kTma, kGroups>);
+    return x != cudaSuccess
+               ? x
+               : cudaFuncSetAttribute(attend_tc_kernel<NT, D, kTma, kGroups>,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
   });
   if (e != cudaSuccess) return e;
   CUtensorMap kmap = {}, vmap = {};

@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kPageThreads) resize_kernel(ResizeArgs a) {
   };
   if (tid == 0) given = 0;
   pdl_wait();
+  pdl_trigger();
   // a sequence's pages before the call, and those that it needs (-1: absent)
   const auto pages_of = [&](int n, int *held, int64_t *need) {
     const int len = a.lens[n], c = a.in.page_counts[n];
@@ -347,6 +348,7 @@ __global__ void __launch_bounds__(kPageThreads) fork_kernel(ForkArgs a) {
 constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(ForkArgs a) {
   pdl_wait();
+  pdl_trigger();
   const PageCopy c = a.copies[blockIdx.x];
   if (c.count <= 0) return;
   char *base = static_cast<char *>(blockIdx.z ? a.v_pool : a.k_pool) + blockIdx.y * a.layer_bytes;
