@@ -141,6 +141,76 @@ __device__ __forceinline__ float reduce16(float v[16], Op op) {
   return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 16));
 }
 
+// The tiles of keys, or of values, of one CTA: a warp loads them in order.
+template <int D, bool kTma>
+struct Loader {
+  // A lane finds one box (TMA) or four positions (copies) of a tile; the
+  // pages are read one tile ahead, and looked at when needed.
+  static constexpr int kFind = kTma ? 1 : 4, kTile = kTok * D * 2;
+  const int32_t *table;
+  const CUtensorMap *map;
+  const uint16_t *pool;  // the head's first element
+  uint8_t *ring;
+  uint64_t *full;
+  int begin, end, h, boxes, in_tile, sub;
+  int32_t found[kFind];
+
+  __device__ __forceinline__ void start(const AttendArgs &a, int lane) {
+    boxes = kTma ? kTok / a.box : 1;
+    in_tile = kTma ? lane % boxes * a.box : lane;
+    sub = kTma ? lane / boxes : 0;
+    look_up(a, 0);
+  }
+  __device__ __forceinline__ void look_up(const AttendArgs &a, int i) {
+#pragma unroll
+    for (int x = 0; x < kFind; ++x) {
+      const int t = begin + i * kTok + 32 * x + in_tile;
+      found[x] = sub < D / 64 && t < end ? table[t / a.g.page_size] : -1;
+    }
+  }
+  // Tile i into stage `slot`, which is free.
+  __device__ __forceinline__ void load(const AttendArgs &a, int i, int slot, int lane) {
+    const uint32_t dst = smem_addr(ring + slot * kTile);
+    if constexpr (kTma) {
+      // boxes lie inside a page: tiles start at multiples of 128 positions,
+      // and a box divides the page size
+      const int page = found[0] < a.g.num_pages ? found[0] : -1;
+      const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * a.box * 128;
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+      __syncwarp();
+      if (page >= 0)
+        tensor_load(dst + sub * (kTok * 128) + in_tile * 128, map, sub * 64,
+                    (begin + i * kTok + in_tile) % a.g.page_size, page, h, &full[slot]);
+      look_up(a, i + 1);
+    } else {
+      // rows' 16-byte chunks, swizzled by the row as the operands expect
+      constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
+      const int chunk = lane % kLanesPerRow;
+      const uint16_t *from_pool = pool + chunk * 8;
+      const uint32_t to = dst + chunk / 8 * (kTok * 128);
+      int64_t offs[kFind];
+#pragma unroll
+      for (int x = 0; x < kFind; ++x) {
+        const int t = begin + i * kTok + 32 * x + lane;
+        offs[x] = found[x] < 0 || found[x] >= a.g.num_pages
+                      ? -1
+                      : found[x] * a.g.page_stride + (t % a.g.page_size) * a.g.slot_stride;
+      }
+      look_up(a, i + 1);
+#pragma unroll
+      for (int x = 0; x < kFind; ++x)
+#pragma unroll 4
+        for (int s = 0; s < 32; s += kRowsPerStep) {
+          const int from = s + lane / kLanesPerRow, row = 32 * x + from;
+          const int64_t off = __shfl_sync(0xFFFFFFFFu, offs[x], from);
+          copy16(to + row * 128 + ((chunk % 8) ^ (row % 8)) * 16, from_pool + (off < 0 ? 0 : off),
+                 off >= 0);
+        }
+      copy_arrive(&full[slot]);
+    }
+  }
+};
+
 template <int NT, int D, bool kTma, int kGroups>
 __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 1 ? 2 : 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -157,35 +227,6 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   static_assert(sizeof(TcBarriers) <= 640, "");
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  if (tid == 0) {
-    for (int s = 0; s < 3; ++s) {
-      mbar_init(&bars->k_full[s], kTma ? 1 : 32);
-      mbar_init(&bars->v_full[s], kTma ? 1 : 32);
-      mbar_init(&bars->k_free[s], 1);
-      mbar_init(&bars->v_free[s], 1);
-    }
-    for (int b = 0; b < 2; ++b) {
-      for (int g = 0; g < kGroups; ++g) {
-        mbar_init(&bars->group[g].s_full[b], 1);
-        mbar_init(&bars->group[g].p_full[b], kSoft);
-        mbar_init(&bars->group[g].pv_done[b], 1);
-      }
-      mbar_init(&bars->drained[b], 1);
-    }
-    mbar_init(&bars->q_full, kGroups * kSoft);
-    bars->gave_up = 0;
-    bars->fix = 0;
-    for (int w = 0; w < kBlockWords; ++w) bars->fix_tokens[w] = 0;
-    fence_mbar_init();
-  }
-  if (warp == kLoadWarp) tmem_alloc(&bars->tmem, T::kCols);
-  if (kTma && tid == (kLoadWarp + 1) * 32) {
-    prefetch_map(&kmap);
-    prefetch_map(&vmap);
-  }
-  pdl_wait();
-  pdl_trigger();
-
   // full ranges come first, the ends of the longest sequences last
   int id = blockIdx.x;
   const int tile0 = id % row_tiles * (NT * kGroups);  // the CTA's first packed row
@@ -193,11 +234,13 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   const int h = id % a.kv_heads;
   id /= a.kv_heads;
   const int n = id % a.N, split = id / a.N;
+  const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
+  pdl_wait();
+  pdl_trigger();
   const int len = a.g.lens[n];
   const int G = a.q_heads / a.kv_heads;
   const int rows = a.R * G;
   const int32_t *parents = a.parents ? a.parents + (int64_t)n * (a.R - 1) : nullptr;
-  const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
   const int64_t cap = table_capacity(a.g), want = (int64_t)len + a.R;
   const int total = len < 0 ? 0 : (int)(want < cap ? want : cap);  // 0: the sequence is not there
   const Ranges range = total > 0 ? deal(total, a.splits, a.least) : Ranges{0, 0};
@@ -205,78 +248,67 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   const int begin = split < range.units ? split * range.per : total;
   const int end = total - begin < range.per ? total : begin + range.per;
   const int tiles = (end - begin + kTok - 1) / kTok;  // 0: nothing for this CTA
+  // The loaders make their barriers and start; what the others need follows.
+  const bool loads = warp == kLoadWarp || warp == kLoadWarp + 1;
+  const bool keys = (warp - kLoadWarp) % 2 == 0;  // (of the last four warps)
+  const int stages = keys ? T::kKStages : T::kVStages;
+  uint64_t *full = keys ? bars->k_full : bars->v_full, *free = keys ? bars->k_free : bars->v_free;
+  uint8_t *ring = keys ? kring : vring;
+  Loader<D, kTma> loader;
+  if (loads) {
+    if (lane == 0) {
+      for (int s = 0; s < 3; ++s) {
+        mbar_init(&full[s], kTma ? 1 : 32);
+        mbar_init(&free[s], 1);
+      }
+      fence_mbar_init();
+    }
+    __syncwarp();
+    loader.table = table;
+    loader.map = keys ? &kmap : &vmap;
+    loader.pool = static_cast<const uint16_t *>(keys ? a.k : a.v) + (int64_t)h * a.g.head_stride;
+    loader.ring = ring;
+    loader.full = full;
+    loader.begin = begin;
+    loader.end = end;
+    loader.h = h;
+    loader.start(a, lane);
+    for (int i = 0; i < stages && i < tiles; ++i) loader.load(a, i, i, lane);
+  } else if (warp == kLoadWarp + 2) {
+    if (lane == 0) {
+      for (int b = 0; b < 2; ++b) {
+        for (int g = 0; g < kGroups; ++g) {
+          mbar_init(&bars->group[g].s_full[b], 1);
+          mbar_init(&bars->group[g].p_full[b], kSoft);
+          mbar_init(&bars->group[g].pv_done[b], 1);
+        }
+        mbar_init(&bars->drained[b], 1);
+      }
+      mbar_init(&bars->q_full, kGroups * kSoft);
+      bars->gave_up = 0;
+      bars->fix = 0;
+      for (int w = 0; w < kBlockWords; ++w) bars->fix_tokens[w] = 0;
+      fence_mbar_init();
+    }
+    __syncwarp();
+    tmem_alloc(&bars->tmem, T::kCols);
+  }
   __syncthreads();
   const uint32_t tmem = bars->tmem;
   volatile uint32_t *gave_up = &bars->gave_up;
 
   if (tiles > 0 && warp >= kLoadWarp) {
     shrink_registers<T::kLoadRegs>();
-    const bool keys = (warp - kLoadWarp) % 2 == 0;
-    const int stages = keys ? T::kKStages : T::kVStages;
-    uint8_t *ring = keys ? kring : vring;
-    uint64_t *full = keys ? bars->k_full : bars->v_full, *free = keys ? bars->k_free : bars->v_free;
-    if (warp < kLoadWarp + 2) {
-      // ---- loads.  A lane finds one box (TMA) or four positions (copies) of
-      // a tile; the pages are read one tile ahead, and looked at when needed.
-      constexpr int kFind = kTma ? 1 : 4;
-      const int boxes = kTma ? kTok / a.box : 1, in_tile = kTma ? lane % boxes * a.box : lane;
-      const int sub = kTma ? lane / boxes : 0;
-      int32_t found[kFind];
-      const auto look_up = [&](int i) {
-#pragma unroll
-        for (int x = 0; x < kFind; ++x) {
-          const int t = begin + i * kTok + 32 * x + in_tile;
-          found[x] = sub < D / 64 && t < end ? table[t / a.g.page_size] : -1;
-        }
-      };
-      look_up(0);
-      for (int i = 0; i < tiles; ++i) {
+    if (loads) {
+      for (int i = stages; i < tiles; ++i) {
         const int slot = i % stages;
-        const uint32_t dst = smem_addr(ring + slot * T::kTile);
         // the stage is free once the products that read it are done
-        bool ok = i < stages || wait_or_give_up(&free[slot], (i / stages - 1) & 1, gave_up);
+        const bool ok = wait_or_give_up(&free[slot], (i / stages - 1) & 1, gave_up);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        if constexpr (kTma) {
-          // boxes lie inside a page: tiles start at multiples of 128
-          // positions, and a box divides the page size
-          const int page = found[0] < a.g.num_pages ? found[0] : -1;
-          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0)) * a.box * 128;
-          if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
-          __syncwarp();
-          if (page >= 0)
-            tensor_load(dst + sub * (kTok * 128) + in_tile * 128, keys ? &kmap : &vmap, sub * 64,
-                        (begin + i * kTok + in_tile) % a.g.page_size, page, h, &full[slot]);
-          if (i + 1 < tiles) look_up(i + 1);
-        } else {
-          // rows' 16-byte chunks, swizzled by the row as the operands expect
-          constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
-          const int chunk = lane % kLanesPerRow;
-          const uint16_t *pool = static_cast<const uint16_t *>(keys ? a.k : a.v) +
-                                 (int64_t)h * a.g.head_stride + chunk * 8;
-          const uint32_t to = dst + chunk / 8 * (kTok * 128);
-          int64_t offs[kFind];
-#pragma unroll
-          for (int x = 0; x < kFind; ++x) {
-            const int t = begin + i * kTok + 32 * x + lane;
-            offs[x] = found[x] < 0 || found[x] >= a.g.num_pages
-                          ? -1
-                          : found[x] * a.g.page_stride + (t % a.g.page_size) * a.g.slot_stride;
-          }
-          if (i + 1 < tiles) look_up(i + 1);
-#pragma unroll
-          for (int x = 0; x < kFind; ++x)
-#pragma unroll 4
-            for (int s = 0; s < 32; s += kRowsPerStep) {
-              const int from = s + lane / kLanesPerRow, row = 32 * x + from;
-              const int64_t off = __shfl_sync(0xFFFFFFFFu, offs[x], from);
-              copy16(to + row * 128 + ((chunk % 8) ^ (row % 8)) * 16, pool + (off < 0 ? 0 : off),
-                     off >= 0);
-            }
-          copy_arrive(&full[slot]);
-        }
+        loader.load(a, i, slot, lane);
       }
       if (!kTma) copy_wait_all();
-    } else if (lane == 0) {
+    } else {
       // ---- products, issued by one lane
       constexpr uint32_t kScores = product_shape(NT, false, false);
       constexpr uint32_t kValues = product_shape(NT, true, true);
@@ -285,6 +317,44 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
         const int slot = i % stages, b = i & 1, phase = (i >> 1) & 1;
         const uint32_t at = smem_addr(ring + slot * T::kTile);
         ok = wait_or_give_up(&full[slot], (i / stages) & 1, gave_up);
+        const int filled = end - (begin + i * kTok);
+        if (kTma && !keys && ok && filled < kTok) {
+          // what lies behind the range is no value of the sequence, and its
+          // weight of 0 does not hide a NaN
+          uint8_t *v = ring + slot * T::kTile;
+          for (int x = lane; x < (kTok - filled) * (D / 8); x += 32)
+            *reinterpret_cast<uint4 *>(v + x % (D / 8) / 8 * (kTok * 128) +
+                                       (filled + x / (D / 8)) * 128 + x % 8 * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_async_shared();
+        }
+        if (!keys && ok && a.R > 1 && begin + (i + 1) * kTok > len) {
+          // 0 * inf is not 0: values of the block, which some rows must not
+          // see, are taken out if they are not finite, and added at the end
+          const int x0 = begin + i * kTok < len ? len - (begin + i * kTok) : 0;
+          const int x1 = filled < kTok ? filled : kTok;
+          uint8_t *v = ring + slot * T::kTile;
+          bool found = false;
+#pragma unroll 4
+          for (int x = lane; x < (x1 - x0) * (D / 8); x += 32) {
+            const int r = x0 + x / (D / 8), c = x % (D / 8);
+            found |= vec_maybe_nonfinite<uint16_t>(*reinterpret_cast<const uint4 *>(
+                v + c / 8 * (kTok * 128) + r * 128 + ((c % 8) ^ (r % 8)) * 16));
+          }
+          if (__any_sync(0xFFFFFFFFu, found)) {
+            for (int x = lane; x < (x1 - x0) * D; x += 32) {
+              const int r = x0 + x / D, c = x % D / 8, t = begin + i * kTok + r - len;
+              uint16_t *at = reinterpret_cast<uint16_t *>(v + c / 8 * (kTok * 128) + r * 128 +
+                                                          ((c % 8) ^ (r % 8)) * 16) + x % 8;
+              if (!not_finite(*at)) continue;
+              *at = 0;
+              atomicOr(&bars->fix_tokens[t / 32], 1u << (t % 32));
+              bars->fix = 1;
+            }
+            __threadfence_block();
+            fence_async_shared();
+          }
+        }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
           GroupBarriers &bar = bars->group[g];
@@ -294,7 +364,9 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
           } else {
             ok = ok && wait_or_give_up(&bar.p_full[b], phase, gave_up);
           }
+          ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
+          if (lane != 0) continue;
           fence_async_shared();
           tc_fence_after();
           const uint32_t cols = tmem + g * 3 * NT;
@@ -317,9 +389,10 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
             tc_commit(&bar.pv_done[b]);
           }
         }
-        if (ok) tc_commit(&free[slot]);
+        if (ok && lane == 0) tc_commit(&free[slot]);
+        __syncwarp();
       }
-      if (!ok) {  // given up: let what was issued end before tensor memory is freed
+      if (!ok && lane == 0) {  // given up: let what was issued end before tensor memory is freed
         uint64_t *drained = &bars->drained[keys ? 0 : 1];
         tc_commit(drained);
         mbar_wait_bounded(drained, 0);
@@ -447,12 +520,16 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
             float s[16];
             tmem_ld16(scores + c, s);
             tmem_wait_ld16(s);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float x = s[j] * a.scale2;
+              s[j] = fabsf(x) < -kUnset ? -x : -kUnset;
+            }
             if (lane == 0) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float x = s[j] * a.scale2;
-                nrefs[c + j] = fabsf(x) < -kUnset ? -x : -kUnset;
-              }
+              for (int j = 0; j < 16; j += 4)
+                *reinterpret_cast<float4 *>(nrefs + c + j) =
+                    make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
             }
           }
         }
@@ -514,45 +591,19 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       for (int c = 0; c < NT / 2; c += 4)
         *reinterpret_cast<uint4 *>(pt + c / 4 * 2048) =
             make_uint4(packed[c], packed[c + 1], packed[c + 2], packed[c + 3]);
-      if (masked && !there) {
-        // what lies here is no value of the sequence: 0 * NaN is not 0
+      if (kTma && bad_page && t < end && !there) {  // (nor is what lies in place of a bad page)
         const int slot = i % T::kVStages;
         wait_or_give_up(&bars->v_full[slot], (i / T::kVStages) & 1, gave_up);
         uint8_t *v = vring + slot * T::kTile + st * 128;
         for (int c = 0; c < D / 8; ++c)
           *reinterpret_cast<uint4 *>(v + c / 8 * (kTok * 128) + c % 8 * 16) = make_uint4(0, 0, 0, 0);
       }
-      if (a.R > 1 && there && t >= len) {
-        // 0 * inf is not 0: a value of the block that some rows must not see
-        // is taken out here if it is not finite, and added at the end
-        const int slot = i % T::kVStages;
-        wait_or_give_up(&bars->v_full[slot], (i / T::kVStages) & 1, gave_up);
-        uint8_t *v = vring + slot * T::kTile + st * 128;
-        bool fix = false;
-        for (int c = 0; c < D / 8; ++c) {
-          uint16_t *at = reinterpret_cast<uint16_t *>(v + c / 8 * (kTok * 128) +
-                                                      ((c % 8) ^ (st % 8)) * 16);
-          if (!vec_maybe_nonfinite<uint16_t>(*reinterpret_cast<const uint4 *>(at))) continue;
-          for (int k = 0; k < 8; ++k)
-            if (not_finite(at[k])) {
-              fix = true;
-              at[k] = 0;
-            }
-        }
-        if (fix) {
-          atomicOr(&bars->fix_tokens[(t - len) / 32], 1u << ((t - len) % 32));
-          bars->fix = 1;
-        }
-      }
       tc_fence_before();
       fence_async_shared();
       mbar_arrive(&bar.p_full[i & 1]);
     }
 
-    // ---- results
-    wait_or_give_up(&bar.pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, gave_up);
-    __syncwarp();
-    tc_fence_after();
+    // ---- results: the sums while the last product runs
 #pragma unroll
     for (int c = 0; c < NT; c += 16) {  // add up the lanes
       const float sum = reduce16(l + c, [](float x, float y) { return x + y; });
@@ -574,14 +625,19 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       }
     }
     named_sync(sync, kSoft);
+    wait_or_give_up(&bar.pv_done[(tiles - 1) & 1], ((tiles - 1) >> 1) & 1, gave_up);
+    __syncwarp();
+    tc_fence_after();
     const int d = st;  // O^T: one thread per element of the head
     const bool fix = bars->fix;
     uint16_t *staged = reinterpret_cast<uint16_t *>(q_own);  // (Q has been read)
-#pragma unroll 1
-    for (int c = 0; c < NT && row0 + c < rows; c += 16) {
-      float o[16];
-      tmem_ld16(own + 2 * NT + c, o);
+    float ahead[2][16];
+    tmem_ld16(own + 2 * NT, ahead[0]);
+#pragma unroll
+    for (int c = 0; c < NT; c += 16) {
+      float *o = ahead[c / 16 % 2];
       tmem_wait_ld16(o);
+      if (c + 16 < NT) tmem_ld16(own + 2 * NT + c + 16, ahead[1 - c / 16 % 2]);
       if (d >= D) continue;
       if (fix) {
         for (int x = 0; x < a.R; ++x) {
@@ -590,10 +646,11 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
           const uint16_t v =
               static_cast<const uint16_t *>(a.v)[off + (int64_t)h * a.g.head_stride + d];
           // (times its weight it is what it is)
+          if (!not_finite(v)) continue;
           const uint32_t seers = desc[x * T::kMaskWords + c / 32] >> (c % 32);
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (not_finite(v) && ((seers >> j) & 1u)) o[j] += Elem<uint16_t>::to_float(v);
+            if ((seers >> j) & 1u) o[j] += Elem<uint16_t>::to_float(v);
         }
       }
       float f[16];
@@ -618,17 +675,18 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     }
     if (!joined) {
       named_sync(sync, kSoft);
-      for (int i = st; i < NT * D / 8; i += kSoft) {
-        const int j = i / (D / 8), c = i % (D / 8) * 8;
+#pragma unroll
+      for (int x = 0; x < NT * D / 8 / kSoft; ++x) {
+        const int i = st + x * kSoft, j = i / (D / 8), c = i % (D / 8) * 8;
+        const uint4 v = *reinterpret_cast<const uint4 *>(staged + j * D + c);
         if (row0 + j < rows)
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out_o) + out_at[j] + c) =
-              *reinterpret_cast<const uint4 *>(staged + j * D + c);
+          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out_o) + out_at[j] + c) = v;
       }
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kLoadWarp) {
+  if (warp == kLoadWarp + 2) {
     tc_fence_after();
     tmem_free(tmem, T::kCols);
   }
