@@ -72,10 +72,12 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   id /= row_tiles;
   const int h = id % a.kv_heads;
   id /= a.kv_heads;
-  const int n = id % a.N, split = id / a.N;
+  int n = id % a.N;
+  const int split = id / a.N;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   pdl_wait();
   pdl_trigger();
+  if (a.ordered) n = nth_longest(a.g.lens, a.N, n);
   const int len = a.g.lens[n];
   if (len < 0) return;  // the sequence is not there
   const int rows = a.R * G;
@@ -364,17 +366,19 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
   if (p.tc) attend_tc_rows(rows, &p);
   p.row_tiles = (rows + p.rows - 1) / p.rows;
   const int64_t base = (int64_t)N * kv_heads * p.row_tiles;
-  // CTAs that the device holds at once.  A short batch is dealt out to about
-  // two of them each; a long one in ranges of at least 8 tiles, a quarter of
-  // an SM's share each, so that ragged lengths even out.  The table's width
-  // bounds the lengths; shorter sequences get shorter ranges (`least`).
+  // CTAs that the device holds at once, and a sequence's tiles by the table's
+  // width.  A range is an SM's even share of all that the tables could hold:
+  // a CTA costs about as much as five tiles beyond its own (finer ranges, for
+  // two to six CTAs in turn, took up to 30 % longer).  Where there are few
+  // sequences, those far shorter than their tables get shorter ranges.
   const int64_t fill = (int64_t)device_sm_count() * (!p.tc ? 4 : p.groups == 1 ? 2 : 1);
   const int64_t tiles = (capacity + kPosTile - 1) / kPosTile;
-  const auto share = [&](int64_t waves) { return (tiles * base + waves * fill - 1) / (waves * fill); };
-  const int64_t per = share(2) <= 8 ? std::max<int64_t>(share(2), 1) : std::max<int64_t>(share(4), 8);
-  p.least = (int32_t)std::min<int64_t>(8, (16 * base + fill - 1) / fill);
+  const int64_t per = std::max<int64_t>(1, (tiles * base + fill - 1) / fill);
+  p.least = (int32_t)(2 * base >= fill ? per : std::min<int64_t>(8, (32 * base + fill - 1) / fill));
   p.splits = (int32_t)std::min<int64_t>((tiles + per - 1) / per, kMaxSplits);
   p.ctas = base * p.splits;
+  // few enough CTAs that the order of ragged lengths decides when the last one ends
+  p.ordered = N > 1 && N <= kOrdered && p.ctas < 8 * fill;
   const size_t parts = (size_t)N * R * q_heads * p.splits;
   p.workspace = p.splits > 1 ? parts * (sizeof(float) * D + sizeof(float2)) : 0;
   return p;
@@ -384,6 +388,7 @@ cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan,
                           cudaStream_t stream) {
   a.splits = plan.splits;
   a.least = plan.least;
+  a.ordered = plan.ordered;
   if (plan.ctas > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   const size_t parts = (size_t)a.N * a.R * a.q_heads * plan.splits;
   a.part_o = static_cast<float *>(workspace);

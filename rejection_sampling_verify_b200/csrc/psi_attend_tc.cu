@@ -227,16 +227,18 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   static_assert(sizeof(TcBarriers) <= 640, "");
 
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  // full ranges come first, the ends of the longest sequences last
+  // first ranges come first, of the longest sequences before the others
   int id = blockIdx.x;
   const int tile0 = id % row_tiles * (NT * kGroups);  // the CTA's first packed row
   id /= row_tiles;
   const int h = id % a.kv_heads;
   id /= a.kv_heads;
-  const int n = id % a.N, split = id / a.N;
-  const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
+  int n = id % a.N;
+  const int split = id / a.N;
   pdl_wait();
   pdl_trigger();
+  if (a.ordered) n = nth_longest(a.g.lens, a.N, n);
+  const int32_t *table = a.g.table + (int64_t)n * a.g.max_pages;
   const int len = a.g.lens[n];
   const int G = a.q_heads / a.kv_heads;
   const int rows = a.R * G;

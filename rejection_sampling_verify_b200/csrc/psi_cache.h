@@ -7,6 +7,26 @@
 
 namespace psi {
 
+#ifdef __CUDACC__
+// The sequence with the k-th longest length (of two alike, the lower index
+// first), found by each warp for itself: two lengths a lane.
+constexpr int kOrdered = 64;
+__device__ __forceinline__ int nth_longest(const int32_t *lens, int N, int k) {
+  const int lane = threadIdx.x % 32;
+  const int32_t v0 = lane < N ? lens[lane] : INT32_MIN;
+  const int32_t v1 = lane + 32 < N ? lens[lane + 32] : INT32_MIN;
+  int before0 = 0, before1 = 0;  // lengths that come before this lane's
+  for (int u = 0; u < N; ++u) {
+    const int32_t x = __shfl_sync(0xFFFFFFFFu, u < 32 ? v0 : v1, u % 32);
+    before0 += x > v0 || (x == v0 && u < lane);
+    before1 += x > v1 || (x == v1 && u < lane + 32);
+  }
+  const uint32_t is0 = __ballot_sync(0xFFFFFFFFu, lane < N && before0 == k);
+  const uint32_t is1 = __ballot_sync(0xFFFFFFFFu, lane + 32 < N && before1 == k);
+  return is0 ? __ffs(is0) - 1 : 31 + __ffs(is1);
+}
+#endif
+
 // A block's queries against one layer's pages.
 struct AttendArgs {
   Paging g;
@@ -23,6 +43,7 @@ struct AttendArgs {
   // second kernel
   int32_t splits;  // ranges of a sequence at most
   int32_t least;   // tiles of a range at least
+  int32_t ordered; // CTAs take the longest sequences first (N <= kOrdered)
   float *part_o;   // [N * R * q_heads][splits][D], relative to part_ml's maximum
   float2 *part_ml; // [N * R * q_heads][splits]: maximum (log2 units), sum
   int32_t box;     // positions per TMA box
@@ -31,7 +52,7 @@ struct AttendPlan {
   bool tc;        // on the tensor cores
   int32_t rows;   // packed rows per CTA
   int32_t groups; // of softmax warps per CTA (tensor cores)
-  int32_t splits, least, row_tiles;
+  int32_t splits, least, row_tiles, ordered;
   int64_t ctas;
   size_t workspace;
 };

@@ -99,7 +99,7 @@ PSI_HD Ranges deal(int32_t total, int32_t splits, int32_t least) {
   if (per < least) per = least;
   Ranges r;
   r.units = (tiles - 1) / per + 1;
-  r.per = per * kPosTile;
+  r.per = ((tiles - 1) / r.units + 1) * kPosTile;  // evenly
   return r;
 }
 
