@@ -8,8 +8,10 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "psi_cache.h"
+#include "psi_tcgen05.cuh"
 
 namespace psi {
 namespace {
@@ -55,17 +57,38 @@ __device__ __forceinline__ float4 lds4(const float *p) {
   return *reinterpret_cast<const float4 *>(p);
 }
 
-// Any head size, both element types: products in float on the FMA pipe.
+// Four elements of shared memory as floats.
 template <typename Bits>
+__device__ __forceinline__ float4 four(const Bits *p) {
+  if constexpr (sizeof(Bits) == 2) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
+  } else {
+    return *reinterpret_cast<const float4 *>(p);
+  }
+}
+
+// A row of a tile in shared memory: an odd number of 16-byte vectors, so that
+// 32 lanes that read one row each meet all banks.
+__host__ __device__ inline int row_bytes(int D, int elem) {
+  const int vecs = D * elem / 16;
+  return (vecs | 1) * 16 == vecs * 16 ? (vecs + 2) * 16 : (vecs | 1) * 16;
+}
+
+// Any head size, both element types: products in float on the FMA pipe.  A
+// warp keeps four packed rows: a lane takes one of 32 positions for the
+// scores, and four (or eight) elements of the head for the results.  Keys and
+// values of the next 32 positions are copied while these are at work.
+template <typename Bits, int kChunks>
 __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int32_t row_tiles) {
-  extern __shared__ __align__(16) float smem[];
-  const int D = a.D, G = a.q_heads / a.kv_heads, KS = D + 4;
-  float *qs = smem;                           // [kRowTile][D]
-  float *ks = qs + kRowTile * D;              // [kTokTile][D + 4]
-  float *vs = ks + kTokTile * KS;             // [kTokTile][D]
-  float *ps = vs + kTokTile * D;              // [4 warps][kTokTile][4 rows]
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int D = a.D, G = a.q_heads / a.kv_heads, pitch = row_bytes(D, sizeof(Bits));
+  float *qs = reinterpret_cast<float *>(smem_raw);           // [kRowTile][D]
+  float *ps = qs + kRowTile * D;                             // [4 warps][kTokTile][4 rows]
+  uint8_t *tiles = reinterpret_cast<uint8_t *>(ps + 4 * kTokTile * 4);  // [2][keys, values][kTokTile]
   __shared__ uint32_t sees[kRowTile][kBlockWords];
-  __shared__ int64_t offs[kTokTile];
+  __shared__ bool valid[2][kTokTile];
 
   int id = blockIdx.x;
   const int tile = id % row_tiles;
@@ -86,11 +109,31 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
   const int64_t cap = table_capacity(a.g);
   const int64_t want = (int64_t)len + a.R;
   const int T = (int)(want < cap ? want : cap);
-  const Ranges range = deal(T, a.splits, a.least);
+  const Ranges range = deal(T, a.tile, a.splits, a.least);
   if (split >= range.units) return;
   const int begin = split * range.per;
   const int end = T - begin < range.per ? T : begin + range.per;
   if (want > cap && a.dev_status && tid == 0) atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
+
+  // four threads copy a position's key and value, every fourth vector each
+  const int mine = tid / 4, vecs = D * (int)sizeof(Bits) / 16;
+  const auto copy = [&](int t0, int stage) {
+    const int t = t0 + mine;
+    const int64_t off = t < end ? slot_offset(a.g, table, t) : -1;
+    if (tid % 4 == 0) {
+      valid[stage][mine] = off >= 0;
+      if (t < end && off < 0 && a.dev_status) atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
+    }
+    const int64_t at = (off < 0 ? 0 : off + (int64_t)h * a.g.head_stride) * (int)sizeof(Bits);
+    const uint8_t *k = static_cast<const uint8_t *>(a.k) + at, *v = static_cast<const uint8_t *>(a.v) + at;
+    const uint32_t to = smem_addr(tiles + (size_t)stage * 2 * kTokTile * pitch + mine * pitch);
+    for (int c = tid % 4; c < vecs; c += 4) {
+      copy16(to + c * 16, k + c * 16, off >= 0);
+      copy16(to + kTokTile * pitch + c * 16, v + c * 16, off >= 0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  copy(begin, 0);
 
   for (int i = tid; i < kRowTile; i += kSimtThreads) {
     const int pr = tile * kRowTile + i;
@@ -109,62 +152,52 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
                   f);
     for (int k = 0; k < 8; ++k) qs[r * D + c + k] = f[k] * a.scale2;
   }
-  __syncthreads();
 
-  float m[4], l[4], acc[4][8];
+  // this lane's elements of the head (those past its end repeat its first)
+  int dim[kChunks];
+#pragma unroll
+  for (int c = 0; c < kChunks; ++c) dim[c] = lane * 4 + c * 128 < D ? lane * 4 + c * 128 : 0;
+  float m[4], l[4], acc[4][4 * kChunks];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     m[i] = kNegInf;
     l[i] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
+    for (int k = 0; k < 4 * kChunks; ++k) acc[i][k] = 0.f;
   }
-  // bit 0 of sees[][0] is the root: set for every row that belongs to the block
-  bool live[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) live[i] = sees[warp * 4 + i][0] & 1u;
   const float *qrow = qs + warp * 4 * D;
   float *prow = ps + warp * kTokTile * 4;
 
-  for (int t0 = begin; t0 < end; t0 += kTokTile) {
-    if (tid < kTokTile) {
-      const int t = t0 + tid;
-      const int64_t o = t < end ? slot_offset(a.g, table, t) : -1;
-      if (t < end && o < 0 && a.dev_status) atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
-      offs[tid] = o;
+  int stage = 0;
+  for (int t0 = begin; t0 < end; t0 += kTokTile, stage ^= 1) {
+    if (t0 + kTokTile < end) {
+      copy(t0 + kTokTile, stage ^ 1);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    for (int i = tid; i < kTokTile * D / 8; i += kSimtThreads) {
-      const int t = i / (D / 8), c = i % (D / 8) * 8;
-      float fk[8] = {}, fv[8] = {};
-      if (offs[t] >= 0) {
-        const int64_t at = offs[t] + (int64_t)h * a.g.head_stride + c;
-        load8<Bits>(a.k, at, fk);
-        load8<Bits>(a.v, at, fv);
-      }
-      for (int k = 0; k < 8; ++k) {
-        ks[t * KS + c + k] = fk[k];
-        vs[t * D + c + k] = fv[k];
-      }
-    }
-    __syncthreads();
+    const uint8_t *ks = tiles + (size_t)stage * 2 * kTokTile * pitch, *vs = ks + kTokTile * pitch;
+    const Bits *key = reinterpret_cast<const Bits *>(ks + lane * pitch);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-      const float4 kk = lds4(ks + lane * KS + d);
+      const float4 kk = four<Bits>(key + d);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float4 q4 = lds4(qrow + i * D + d);
         s[i] = fmaf(q4.x, kk.x, fmaf(q4.y, kk.y, fmaf(q4.z, kk.z, fmaf(q4.w, kk.w, s[i]))));
       }
     }
-    const int t = t0 + lane, back = t - len;
-    const bool there = t < end && offs[lane] >= 0;
+    const int back = t0 + lane - len;
+    const bool there = valid[stage][lane];
     float scale[4];
+    bool all = true;  // the position is seen by the warp's four rows
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool seen =
-          there && live[i] &&
-          (back < 0 || ((sees[warp * 4 + i][back >> 5] >> (back & 31)) & 1u));
+      // (bit 0, the root, is set for every row that belongs to the block)
+      const uint32_t *row = sees[warp * 4 + i];
+      const bool seen = there && (back < 0 ? row[0] & 1u : (row[back >> 5] >> (back & 31)) & 1u);
       const float x = seen ? s[i] : kNegInf;
       const float top = fmaxf(m[i], warp_max(x));
       // nothing seen so far: keep the weights at zero rather than inf - inf
@@ -174,31 +207,37 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
       l[i] = l[i] * scale[i] + warp_sum(p);
       m[i] = top;
       prow[lane * 4 + i] = seen ? p : -1.f;
+      all &= seen;
     }
-    __syncwarp();
+    all = __all_sync(0xFFFFFFFFu, all);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc[i][k] *= scale[i];
-    const int last = end - t0 < kTokTile ? end - t0 : kTokTile;
-    for (int j = 0; j < last; ++j) {
-      const float4 p4 = lds4(prow + j * 4);
-      const float p[4] = {p4.x, p4.y, p4.z, p4.w};
+      for (int k = 0; k < 4 * kChunks; ++k) acc[i][k] *= scale[i];
+    const auto values = [&](auto whole) {
+      const int last = end - t0 < kTokTile ? end - t0 : kTokTile;
+#pragma unroll 8
+      for (int j = 0; j < (whole.value ? kTokTile : last); ++j) {
+        const float4 p4 = lds4(prow + j * 4);
+        const float p[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int d = lane * 4 + c * 128;
-        if (d >= D) continue;
-        const float4 v4 = lds4(vs + j * D + d);
+        for (int c = 0; c < kChunks; ++c) {
+          const float4 v4 = four<Bits>(reinterpret_cast<const Bits *>(vs + j * pitch) + dim[c]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (p[i] < 0.f) continue;  // not seen: it may be inf or NaN
-          acc[i][c * 4 + 0] = fmaf(p[i], v4.x, acc[i][c * 4 + 0]);
-          acc[i][c * 4 + 1] = fmaf(p[i], v4.y, acc[i][c * 4 + 1]);
-          acc[i][c * 4 + 2] = fmaf(p[i], v4.z, acc[i][c * 4 + 2]);
-          acc[i][c * 4 + 3] = fmaf(p[i], v4.w, acc[i][c * 4 + 3]);
+          for (int i = 0; i < 4; ++i) {
+            // what is not seen (p = -1) may be inf or NaN
+            const bool on = whole.value || !(p[i] < 0.f);
+            float *x = acc[i] + c * 4;
+            x[0] = on ? fmaf(p[i], v4.x, x[0]) : x[0];
+            x[1] = on ? fmaf(p[i], v4.y, x[1]) : x[1];
+            x[2] = on ? fmaf(p[i], v4.z, x[2]) : x[2];
+            x[3] = on ? fmaf(p[i], v4.w, x[3]) : x[3];
+          }
         }
       }
-    }
+    };
+    if (all) values(std::true_type{});
+    else values(std::false_type{});
     __syncthreads();
   }
 
@@ -211,7 +250,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
       const int64_t at = row * a.splits + split;
       if (lane == 0) a.part_ml[at] = make_float2(m[i], l[i]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < kChunks; ++c) {
         const int d = lane * 4 + c * 128;
         if (d < D)
           *reinterpret_cast<float4 *>(a.part_o + at * D + d) =
@@ -222,7 +261,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
       const float inv = any ? 1.f / l[i] : 0.f;
       if (lane == 0 && a.out_lse) a.out_lse[row] = any ? m[i] * kLn2 + logf(l[i]) : kNegInf;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 0; k < 4 * kChunks; ++k) {
         const int d = lane * 4 + k / 4 * 128 + k % 4;
         if (d < D)
           Store<Bits>::put(a.out_o, row * D + d, any ? acc[i][k] * inv : 0.f);
@@ -249,7 +288,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
   const int len = a.g.lens[row / ((int64_t)a.R * a.q_heads)];
   if (len < 0) return;
   const int64_t cap = table_capacity(a.g), want = (int64_t)len + a.R;
-  const int units = deal((int)(want < cap ? want : cap), a.splits, a.least).units;
+  const int units = deal((int)(want < cap ? want : cap), a.tile, a.splits, a.least).units;
   if (units == 1) return;  // (the row is written already)
   const float2 *ml = a.part_ml + row * a.splits;
   float top = kNegInf;
@@ -319,24 +358,24 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(AttendArgs a) {
   }
 }
 
-size_t simt_smem(int D) {
-  return sizeof(float) *
-         ((size_t)kRowTile * D + (size_t)kTokTile * (D + 4) + (size_t)kTokTile * D + 4 * kTokTile * 4);
+size_t simt_smem(int D, int elem) {
+  return sizeof(float) * ((size_t)kRowTile * D + 4 * kTokTile * 4) +
+         (size_t)2 * 2 * kTokTile * row_bytes(D, elem);
 }
 
-template <typename Bits>
+template <typename Bits, int kChunks>
 cudaError_t launch_simt(const AttendArgs &a, const AttendPlan &plan, cudaStream_t stream) {
   static DeviceOnce once;
   const cudaError_t e = once([] {
-    const cudaError_t x = prefer_max_shared(attend_kernel<Bits>);
-    return x != cudaSuccess
-               ? x
-               : cudaFuncSetAttribute(attend_kernel<Bits>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)simt_smem(PSI_MAX_HEAD_DIM));
+    const cudaError_t x = prefer_max_shared(attend_kernel<Bits, kChunks>);
+    return x != cudaSuccess ? x
+                            : cudaFuncSetAttribute(attend_kernel<Bits, kChunks>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)simt_smem(128 * kChunks, sizeof(Bits)));
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(attend_kernel<Bits>, dim3((unsigned)plan.ctas), dim3(kSimtThreads),
-                    simt_smem(a.D), stream, a, plan.row_tiles);
+  return launch_pdl(attend_kernel<Bits, kChunks>, dim3((unsigned)plan.ctas), dim3(kSimtThreads),
+                    simt_smem(a.D, sizeof(Bits)), stream, a, plan.row_tiles);
 }
 
 template <typename Bits>
@@ -371,10 +410,11 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
   // a CTA costs about as much as five tiles beyond its own (finer ranges, for
   // two to six CTAs in turn, took up to 30 % longer).  Where there are few
   // sequences, those far shorter than their tables get shorter ranges.
-  const int64_t fill = (int64_t)device_sm_count() * (!p.tc ? 4 : p.groups == 1 ? 2 : 1);
-  const int64_t tiles = (capacity + kPosTile - 1) / kPosTile;
+  const int64_t fill = (int64_t)device_sm_count() * (!p.tc ? 8 : p.groups == 1 ? 2 : 1);
+  p.tile = p.tc ? kTcTile : 2 * kTokTile;
+  const int64_t tiles = (capacity + p.tile - 1) / p.tile;
   const int64_t per = std::max<int64_t>(1, (tiles * base + fill - 1) / fill);
-  p.least = (int32_t)(2 * base >= fill ? per : std::min<int64_t>(8, (32 * base + fill - 1) / fill));
+  p.least = (int32_t)(2 * base >= fill ? per : std::min<int64_t>(8, ((p.tc ? 32 : 8) * base + fill - 1) / fill));
   p.splits = (int32_t)std::min<int64_t>((tiles + per - 1) / per, kMaxSplits);
   p.ctas = base * p.splits;
   // few enough CTAs that the order of ragged lengths decides when the last one ends
@@ -386,6 +426,7 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
 
 cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan, void *workspace,
                           cudaStream_t stream) {
+  a.tile = plan.tile;
   a.splits = plan.splits;
   a.least = plan.least;
   a.ordered = plan.ordered;
@@ -394,9 +435,12 @@ cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan,
   a.part_o = static_cast<float *>(workspace);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + parts * a.D);
   const bool bf16 = dtype == PSI_DTYPE_BF16;
-  const cudaError_t e = plan.tc ? launch_attend_tc(a, plan, stream)
-                        : bf16  ? launch_simt<uint16_t>(a, plan, stream)
-                                : launch_simt<uint32_t>(a, plan, stream);
+  const cudaError_t e =
+      plan.tc      ? launch_attend_tc(a, plan, stream)
+      : a.D <= 128 ? (bf16 ? launch_simt<uint16_t, 1>(a, plan, stream)
+                           : launch_simt<uint32_t, 1>(a, plan, stream))
+                   : (bf16 ? launch_simt<uint16_t, 2>(a, plan, stream)
+                           : launch_simt<uint32_t, 2>(a, plan, stream));
   if (e != cudaSuccess || a.splits == 1) return e;
   return bf16 ? launch_join<uint16_t>(a, stream) : launch_join<uint32_t>(a, stream);
 }

@@ -40,7 +40,7 @@
 namespace psi {
 namespace {
 
-constexpr int kTok = kPosTile;  // positions per tile
+constexpr int kTok = kTcTile;  // positions per tile
 constexpr int kSoft = 128;  // softmax threads of a group
 constexpr float kUnset = -1e30f;   // no reference yet
 constexpr float kHeadroom = 60.f;  // log2 units a score may exceed its reference by
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   const int32_t *parents = a.parents ? a.parents + (int64_t)n * (a.R - 1) : nullptr;
   const int64_t cap = table_capacity(a.g), want = (int64_t)len + a.R;
   const int total = len < 0 ? 0 : (int)(want < cap ? want : cap);  // 0: the sequence is not there
-  const Ranges range = total > 0 ? deal(total, a.splits, a.least) : Ranges{0, 0};
+  const Ranges range = total > 0 ? deal(total, kTok, a.splits, a.least) : Ranges{0, 0};
   const bool joined = range.units > 1;
   const int begin = split < range.units ? split * range.per : total;
   const int end = total - begin < range.per ? total : begin + range.per;

@@ -41,6 +41,7 @@ struct AttendArgs {
   uint32_t *dev_status;
   // a long sequence is dealt to several CTAs: partial results, joined by a
   // second kernel
+  int32_t tile;    // positions of a tile
   int32_t splits;  // ranges of a sequence at most
   int32_t least;   // tiles of a range at least
   int32_t ordered; // CTAs take the longest sequences first (N <= kOrdered)
@@ -52,7 +53,7 @@ struct AttendPlan {
   bool tc;        // on the tensor cores
   int32_t rows;   // packed rows per CTA
   int32_t groups; // of softmax warps per CTA (tensor cores)
-  int32_t splits, least, row_tiles, ordered;
+  int32_t tile, splits, least, row_tiles, ordered;
   int64_t ctas;
   size_t workspace;
 };
@@ -61,7 +62,8 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
 cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan, void *workspace,
                           cudaStream_t stream);
 
-// The tensor-core form (psi_attend_tc.cu).
+// The tensor-core form (psi_attend_tc.cu), on tiles of kTcTile positions.
+constexpr int kTcTile = 128;
 bool attend_tc_fits(psi_dtype dtype, int32_t D);
 void attend_tc_rows(int rows, AttendPlan *p);
 cudaError_t launch_attend_tc(AttendArgs a, const AttendPlan &plan, cudaStream_t stream);

@@ -87,19 +87,18 @@ PSI_HD int32_t path_prefix(const int32_t *nodes, int32_t len, int32_t M) {
 }
 
 // How a sequence's positions are dealt to the CTAs of its rows: `units`
-// ranges of `per` positions (a multiple of the tile of 128), at most `splits`
-// of them and none below `least` tiles.
-constexpr int kPosTile = 128;
+// ranges of `per` positions (a multiple of the tile), at most `splits` of
+// them and none below `least` tiles.
 struct Ranges {
   int32_t units, per;
 };
-PSI_HD Ranges deal(int32_t total, int32_t splits, int32_t least) {
-  const int32_t tiles = (total - 1) / kPosTile + 1;
+PSI_HD Ranges deal(int32_t total, int32_t tile, int32_t splits, int32_t least) {
+  const int32_t tiles = (total - 1) / tile + 1;
   int32_t per = (tiles - 1) / splits + 1;
   if (per < least) per = least;
   Ranges r;
   r.units = (tiles - 1) / per + 1;
-  r.per = ((tiles - 1) / r.units + 1) * kPosTile;  // evenly
+  r.per = ((tiles - 1) / r.units + 1) * tile;  // evenly
   return r;
 }
 
