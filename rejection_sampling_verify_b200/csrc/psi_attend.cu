@@ -430,7 +430,6 @@ cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan,
   a.splits = plan.splits;
   a.least = plan.least;
   a.ordered = plan.ordered;
-  if (plan.ctas > 0x7FFFFFFFLL) return cudaErrorInvalidConfiguration;
   const size_t parts = (size_t)a.N * a.R * a.q_heads * plan.splits;
   a.part_o = static_cast<float *>(workspace);
   a.part_ml = reinterpret_cast<float2 *>(a.part_o + parts * a.D);

@@ -562,7 +562,8 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
                                 fmaxf(wred[2 * NT + st], wred[3 * NT + st]));
           // (each row by its own scores: what other rows see does not touch its bits)
           const float old = -nrefs[st], now = m > old + kHeadroom ? m : old;
-          facs[st] = now == old && i > 0 ? 1.f : fast_exp2(old - now);
+          // (the first tile's weights are in no sum yet: nothing is kept)
+          facs[st] = i == 0 ? 0.f : now == old ? 1.f : fast_exp2(old - now);
           nrefs[st] = -now;
         }
         if (i > 0) wait_or_give_up(&bar.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
@@ -645,6 +646,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
         for (int x = 0; x < a.R; ++x) {
           if (!((bars->fix_tokens[x / 32] >> (x % 32)) & 1u)) continue;
           const int64_t off = slot_offset(a.g, table, (int64_t)len + x);
+          if (off < 0) continue;  // (what lay in place of a bad page was seen by nobody)
           const uint16_t v =
               static_cast<const uint16_t *>(a.v)[off + (int64_t)h * a.g.head_stride + d];
           // (times its weight it is what it is)

@@ -77,8 +77,8 @@ psi_status check_block(const psi_cache_layout *c, int32_t N, int32_t R, int32_t 
   if (q_heads % c->kv_heads != 0)
     return api_fail(PSI_ERR_INVALID_ARG, "q_heads=%d is not a multiple of kv_heads=%d", q_heads,
                     c->kv_heads);
-  if ((int64_t)N * R > INT32_MAX / 2)
-    return api_fail(PSI_ERR_UNSUPPORTED, "N=%d R=%d: too many rows", N, R);
+  if ((int64_t)N * R > INT32_MAX || (int64_t)N * R * q_heads > INT32_MAX)
+    return api_fail(PSI_ERR_UNSUPPORTED, "N=%d R=%d q_heads=%d: too many rows", N, R, q_heads);
   return PSI_OK;
 }
 
@@ -190,7 +190,7 @@ psi_status psi_cache_append(const psi_cache_layout *layout, void *k_pages, void 
 size_t psi_attend_block_workspace_bytes(const psi_cache_layout *layout, int32_t N, int32_t R,
                                         int32_t q_heads, int32_t max_pages) {
   if (check_layout(layout) != PSI_OK || check_block(layout, N, R, q_heads) != PSI_OK ||
-      max_pages < 1)
+      max_pages < 1 || (int64_t)max_pages * layout->page_size > INT32_MAX - 2 * PSI_MAX_BLOCK_ROWS)
     return 0;
   const size_t need =
       psi::plan_attend(N, R, q_heads, layout->kv_heads, layout->head_dim, layout->dtype,
@@ -219,6 +219,12 @@ psi_status psi_attend_block(const psi_cache_layout *layout, const void *k_pages,
   if (!workspace || workspace_bytes < need || !aligned_to(workspace, 16))
     return api_fail(PSI_ERR_WORKSPACE, "workspace %zu bytes at %p, need %zu (16-byte aligned)",
                     workspace_bytes, workspace, need);
+  const psi::AttendPlan plan =
+      psi::plan_attend(N, R, q_heads, layout->kv_heads, layout->head_dim, layout->dtype,
+                       (int64_t)max_pages * layout->page_size);
+  if (plan.ctas > INT32_MAX)
+    return api_fail(PSI_ERR_UNSUPPORTED, "N=%d R=%d kv_heads=%d: too many rows", N, R,
+                    layout->kv_heads);
   psi::AttendArgs a = {};
   a.g = paging(layout, page_table, max_pages, lens);
   a.k = k_pages;
@@ -236,9 +242,6 @@ psi_status psi_attend_block(const psi_cache_layout *layout, const void *k_pages,
   a.out_o = out_o;
   a.out_lse = out_lse;
   a.dev_status = dev_status;
-  const psi::AttendPlan plan =
-      psi::plan_attend(N, R, q_heads, layout->kv_heads, layout->head_dim, layout->dtype,
-                       (int64_t)max_pages * layout->page_size);
   return launched(psi::launch_attend(a, layout->dtype, plan, workspace,
                                      reinterpret_cast<cudaStream_t>(stream)),
                   "attend launch");

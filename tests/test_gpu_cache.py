@@ -209,6 +209,121 @@ def test_attend_padded_batch_and_bad_pages(dtype):
     assert int(out.status.item()) == psi.PSI_DEV_BAD_PAGE
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S", [16, 5])
+@pytest.mark.parametrize("D", [64, 128, 96])
+def test_attend_bad_pages_inside_a_tree_block(D, S, dtype):
+    """Positions of the block itself lose their page, in pools whose other
+    slots hold NaN and inf: the rows that see them go on without them."""
+    N, R, Hq, H = 3, 40, 6, 2
+    k, v, table, lens = _cache(N, [100, 7, 250], R, H, D, S, dtype, 21)
+    used = torch.zeros(k.shape[:2], dtype=torch.bool)
+    for n in range(N):
+        for t in range(int(lens[n]) + R):
+            used[int(table[n, t // S]), t % S] = True
+    k[~used], v[~used] = math.inf, math.nan
+    q = torch.randn(N, R, Hq, D, generator=_gen(22)).to(DT[dtype])
+    parents = _parents("tree", N, R, 23)
+    for n in range(N):
+        held = int((table[n] >= 0).sum())
+        table[n, held - 2] = -1 if n else k.shape[0] + 3
+        table[n, 0] = -7
+    _check_attend(q, k, v, table, lens, parents, want_status=psi.PSI_DEV_BAD_PAGE)
+
+
+def test_attend_lengths_at_and_past_the_table():
+    """The table ends before, at and inside the block, and far before it."""
+    for dtype in DT:
+        k, v, table, lens = _cache(4, [60, 60, 60, 60], 4, 2, 128, 16, dtype, 24)
+        q = torch.randn(4, 4, 4, 128, generator=_gen(25)).to(DT[dtype])
+        lens = torch.tensor([61, 64, 80, 2**31 - 1], dtype=torch.int32)
+        r = psi.attend_block(q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.cuda())
+        o, _, tol = ref.attend(q, k, v, table, torch.tensor([61, 64, 64, 64]))
+        for n in (0, 1):
+            assert bool(((r.o[n].cpu().double() - o[n]).abs() <= tol[n]).all())
+        # past the table a row sees all 64 positions that the table holds, and nothing else
+        for n in (2, 3):
+            assert bool(((r.o[n].cpu().double() - o[n]).abs() <= tol[n]).all())
+        assert int(r.status.item()) == psi.PSI_DEV_BAD_PAGE
+
+
+def test_attend_a_row_of_nan_leaves_the_others():
+    """A NaN query gives NaN for its row and head alone; a whole row at -inf
+    scores next to finite ones has no weight."""
+    for dtype, D in itertools.product(DT, (64, 128)):
+        k, v, table, lens = _cache(2, [300, 40], 5, 1, D, 16, dtype, 26)
+        q = torch.randn(2, 5, 4, D, generator=_gen(27)).to(DT[dtype])
+        clean = psi.attend_block(q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.cuda()).o
+        q[1, 2, 3, 7] = math.nan
+        o = psi.attend_block(q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.cuda()).o
+        assert bool(torch.isnan(o[1, 2, 3]).all())
+        o[1, 2, 3] = clean[1, 2, 3]
+        assert torch.equal(o, clean)
+
+
+def test_short_and_long_forms_of_a_call_agree():
+    """The compiled binding's calls and those with the caller's own outputs
+    give the same bits, on the default and on another stream."""
+    N, R, Hq, H, D, S, L, P = 3, 5, 8, 2, 128, 16, 2, 40
+    g = _gen(28)
+    qkv = torch.randn(N, R, Hq + 2 * H, D, generator=g).bfloat16().cuda()
+    q, kk, vv = qkv.split((Hq, H, H), dim=2)
+    pages = psi.cache_resize(psi.PageState.empty(N, 8, P),
+                             torch.tensor([20, 3, 50], dtype=torch.int32).cuda(), R, S).pages
+    lens = torch.tensor([20, 3, 50], dtype=torch.int32).cuda()
+    kp, vp = (torch.randn(L, P, S, H, D, generator=g).bfloat16().cuda() for _ in range(2))
+    inv, _ = psi.rope_frequencies(D)
+    path = torch.tensor([[0, 2, -1, -1], [1, 3, -1, -1], [-1] * 4], dtype=torch.int32).cuda()
+    steps = torch.tensor([2, 2, 0], dtype=torch.int32).cuda()
+    src, dst = (torch.tensor([x], dtype=torch.int32).cuda() for x in (2, 1))
+
+    def word():
+        return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def like(s):
+        return psi.PageState(*(torch.empty_like(t) for t in (s.table, s.counts, s.refs, s.free,
+                                                             s.n_free)))
+
+    def run(given, stream=None):
+        k, v = kp.clone(), vp.clone()
+        torch.cuda.synchronize()
+        a = psi.cache_append(q, kk, vv, k[0], v[0], pages.table, lens, inv_freq=inv, stream=stream,
+                             out=psi.AppendResult(torch.empty(N, R, Hq, D, dtype=q.dtype,
+                                                              device="cuda"), word())
+                             if given else None)
+        o = psi.attend_block(a.q, k[0], v[0], pages.table, lens, want_lse=True, stream=stream,
+                             out=psi.AttendResult(torch.empty_like(a.q),
+                                                  torch.empty(N, R, Hq, device="cuda"), word())
+                             if given else None)
+        c = psi.cache_commit(k, v, pages.table, lens, path, steps, stream=stream,
+                             out=psi.CommitResult(torch.empty_like(lens), word()) if given else None)
+        z = psi.cache_resize(pages, c.lens, 0, S, stream=stream,
+                             out=psi.ResizeResult(like(pages), word()) if given else None)
+        gone = c.lens.clone()
+        torch.cuda.synchronize()
+        gone[1] = 0
+        e = psi.cache_resize(z.pages, gone, 0, S, stream=stream).pages
+        f = psi.cache_fork(k, v, e, gone, src, dst, stream=stream,
+                           out=psi.ForkResult(like(e), torch.empty_like(gone), word())
+                           if given else None)
+        torch.cuda.synchronize()
+        assert all(int(x.status.item()) == 0 for x in (a, o, c, z, f))
+        return [a.q, o.o, o.lse, c.lens, z.pages.table, z.pages.refs, f.pages.table, f.pages.counts,
+                f.pages.refs, f.pages.n_free, f.lens, k, v]
+
+    want = run(False)
+    for got in (run(True), run(False, torch.cuda.Stream()), run(True, torch.cuda.Stream())):
+        for x, y in zip(want, got):
+            assert torch.equal(x, y)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for x, y in zip(want, run(False)):
+            assert torch.equal(x, y)
+    with pytest.raises(psi.PsiError):  # what the sizes refuse, refused the same in both forms
+        psi.cache_resize(pages, lens, -1, S)
+    with pytest.raises(ValueError, match="lens"):
+        psi.attend_block(q, kp[0], vp[0], pages.table, lens.long())
+
+
 def test_attend_repeats_and_does_not_depend_on_the_batch():
     """The same call gives the same bits; a sequence's result is the same in
     another place of a batch of the same shape."""
