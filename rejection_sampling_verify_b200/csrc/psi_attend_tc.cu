@@ -42,6 +42,7 @@ namespace {
 
 constexpr int kTok = kTcTile;  // positions per tile
 constexpr int kSoft = 128;  // softmax threads of a group
+constexpr int kTurn = 4;    // named barriers of the groups' turns: 4 and 5
 constexpr float kUnset = -1e30f;   // no reference yet
 constexpr float kHeadroom = 60.f;  // log2 units a score may exceed its reference by
 constexpr float kFar = 1.152921504606847e18f;     // 2^kHeadroom
@@ -476,6 +477,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     float l[NT];  // sums of this thread's positions
 #pragma unroll
     for (int j = 0; j < NT; ++j) l[j] = 0.f;
+    if (kGroups == 2 && g == 1) named_arrive(kTurn, 2 * kSoft);  // the first turn is group 0's
     for (int i = 0; i < tiles; ++i) {
       const int t = begin + i * kTok + st;
       // rows that see this thread's position
@@ -510,6 +512,9 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
         }
         return all.x + all.y;
       };
+      // Two groups take turns at the exponentials: while one is at them, the
+      // other stores its weights and waits for its next scores.
+      if (kGroups == 2) named_sync(kTurn + g, 2 * kSoft);
       using std::false_type;
       using std::true_type;
       // Any score of a row will do for its first reference: that of the first
@@ -540,7 +545,10 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       if (!raise) {
         const float all = masked ? weigh_tile(true_type{}, false_type{})
                                  : weigh_tile(false_type{}, false_type{});
+        if (kGroups == 2 && !(g == 1 && i == tiles - 1)) named_arrive(kTurn + 1 - g, 2 * kSoft);
         raise = named_or(sync, kSoft, !(all <= kFar));
+      } else if (kGroups == 2 && !(g == 1 && i == tiles - 1)) {
+        named_arrive(kTurn + 1 - g, 2 * kSoft);
       }
       if (raise) {
 #pragma unroll 1
