@@ -4,8 +4,9 @@ The work happens in ``libpsi_verify.so`` (hand-written CUDA kernels behind a
 C ABI, declared in ``include/psi_verify.h``).  This module only marshals
 arguments: the raw functions below carry the ABI's names and arguments
 one-for-one (device pointers as integers), and the tensor helpers
-(:func:`verify_linear`, :func:`verify_tree_greedy`, :func:`rng_uniforms`)
-take ``torch`` CUDA tensors, allocate outputs and workspace with torch, and
+(:func:`verify_linear`, :func:`verify_tree_greedy`, :func:`rng_uniforms`, and
+the key-value cache's :func:`cache_append`, :func:`attend_block`,
+:func:`cache_commit`, :func:`cache_resize` and :func:`cache_fork`) take ``torch`` CUDA tensors, allocate outputs and workspace with torch, and
 call the raw functions on the current stream.
 
 There is no fallback: if the library is missing or cannot load, every call
