@@ -6,9 +6,8 @@
 // maximum and sum per row (online softmax) and, when the length is split,
 // leaves a partial result that join_kernel adds up.
 //
-// bf16 heads of 64 and 128 elements run on the tensor cores
-// (psi_attend_tc.cu); float32 and every other head size here, on the FMA
-// pipe: bf16 products of any kind would cost float32 half of its digits.
+// bf16 heads of up to 128 elements run on the tensor cores
+// (psi_attend_tc.cu); float32 and larger heads here, on the FMA pipe: bf16 products of any kind would cost float32 half of its digits.
 // Latency bounds small float32 batches: 4 sequences of up to 2,500 positions,
 // 5 rows of 16 query and 2 kv heads of 64 (5.3 MB), take 28 us.
 #include <math.h>
@@ -134,8 +133,8 @@ __global__ void __launch_bounds__(kSimtThreads) attend_kernel(AttendArgs a, int3
     const uint8_t *k = static_cast<const uint8_t *>(a.k) + at, *v = static_cast<const uint8_t *>(a.v) + at;
     const uint32_t to = smem_addr(tiles + (size_t)stage * 2 * kTokTile * pitch + mine * pitch);
     for (int c = tid % 4; c < vecs; c += 4) {
-      copy16(to + c * 16, k + c * 16, off >= 0);
-      copy16(to + kTokTile * pitch + c * 16, v + c * 16, off >= 0);
+      copy16(to + c * 16, k + c * 16, off >= 0 ? 16 : 0);
+      copy16(to + kTokTile * pitch + c * 16, v + c * 16, off >= 0 ? 16 : 0);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -442,8 +441,7 @@ cudaError_t launch_attend(AttendArgs a, psi_dtype dtype, const AttendPlan &plan,
   const bool bf16 = dtype == PSI_DTYPE_BF16;
   const cudaError_t e =
       plan.tc      ? launch_attend_tc(a, plan, stream)
-      : a.D <= 128 ? (bf16 ? launch_simt<uint16_t, 1>(a, plan, stream)
-                           : launch_simt<uint32_t, 1>(a, plan, stream))
+      : a.D <= 128 ? launch_simt<uint32_t, 1>(a, plan, stream)  // (bf16 is above)
                    : (bf16 ? launch_simt<uint16_t, 2>(a, plan, stream)
                            : launch_simt<uint32_t, 2>(a, plan, stream));
   if (e != cudaSuccess || a.splits == 1) return e;

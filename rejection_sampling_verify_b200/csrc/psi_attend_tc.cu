@@ -56,6 +56,15 @@
 namespace psi {
 namespace {
 
+// D, where a template has it, is the tile's 64 or 128 elements; a head of any
+// multiple of 8 (a.D) lies at its start, and zeros fill the rest: they cost
+// products and shared memory, not traffic.  With the head's elements on the
+// FMA pipe instead, heads of 96 took 2,084 us against 221 for the batch above,
+// 2,947 against 131 for the trees, and one token of 900 positions 15.6
+// against 10.6; heads of 8, which fill an eighth of their tile, 1,334 against
+// 170, 1,856 against 118 and 13.8 against 14.3.  Only sequences of a few
+// positions lose (64 of them, heads of 96: 14.8 against 23.5), by the start
+// and end of this kernel's CTAs, which heads of 128 pay there too.
 constexpr int kTok = kTcTile;  // positions per tile
 constexpr int kSoft = 128;  // softmax threads of a group
 constexpr int kTurn = 4;    // named barriers of the groups' turns: 4 and 5
@@ -203,7 +212,9 @@ struct Loader {
       // rows' 16-byte chunks, swizzled by the row as the operands expect
       constexpr int kLanesPerRow = D / 8, kRowsPerStep = 32 / kLanesPerRow;
       const int chunk = lane % kLanesPerRow;
-      const uint16_t *from_pool = pool + chunk * 8;
+      // the tile's elements past the head are zeros
+      const uint32_t bytes = chunk * 8 < a.D ? 16 : 0;
+      const uint16_t *from_pool = pool + (bytes ? chunk * 8 : 0);
       const uint32_t to = dst + chunk / 8 * (kTok * 128);
       int64_t offs[kFind];
 #pragma unroll
@@ -221,7 +232,7 @@ struct Loader {
           const int from = s + lane / kLanesPerRow, row = 32 * x + from;
           const int64_t off = __shfl_sync(0xFFFFFFFFu, offs[x], from);
           copy16(to + row * 128 + ((chunk % 8) ^ (row % 8)) * 16, from_pool + (off < 0 ? 0 : off),
-                 off >= 0);
+                 off >= 0 ? bytes : 0);
         }
       copy_arrive(&full[slot]);
     }
@@ -436,7 +447,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     if (st < NT) {
       const int pr = row0 + st;
       const int64_t row = ((int64_t)n * a.R + pr / G) * a.q_heads + h * G + pr % G;
-      out_at[st] = (joined ? row * a.splits + split : row) * D;
+      out_at[st] = (joined ? row * a.splits + split : row) * a.D;
     }
     {
       constexpr int kMine = NT * D / 8 / kSoft;
@@ -445,7 +456,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       for (int i = 0; i < kMine; ++i) {
         const int r = (st + i * kSoft) / (D / 8), c = (st + i * kSoft) % (D / 8), pr = row0 + r;
         x[i] = make_uint4(0, 0, 0, 0);
-        if (pr < rows)
+        if (pr < rows && c * 8 < a.D)
           x[i] = *reinterpret_cast<const uint4 *>(
               static_cast<const uint16_t *>(a.q) + ((int64_t)n * a.R + pr / G) * a.q_row_stride +
               (int64_t)(h * G + pr % G) * a.q_head_stride + c * 8);
@@ -644,7 +655,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
                             : wred[st] + wred[NT + st] + wred[2 * NT + st] + wred[3 * NT + st];
       facs[st] = s == 0.f ? 0.f : 1.f / s;
       if (row0 + st < rows) {
-        const int64_t at = out_at[st] / D;
+        const int64_t at = out_at[st] / a.D;
         if (joined)
           a.part_ml[at] = make_float2(s == 0.f ? kMinusInf : -nrefs[st], s);
         else if (a.out_lse)
@@ -665,7 +676,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       float *o = ahead[c / 16 % 2];
       tmem_wait_ld16(o);
       if (c + 16 < NT) tmem_ld16(own + 2 * NT + c + 16, ahead[1 - c / 16 % 2]);
-      if (d >= D) continue;
+      if (d >= a.D) continue;
       if (fix) {
         for (int x = 0; x < a.R; ++x) {
           if (!((bars->fix_tokens[x / 32] >> (x % 32)) & 1u)) continue;
@@ -707,7 +718,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       for (int x = 0; x < NT * D / 8 / kSoft; ++x) {
         const int i = st + x * kSoft, j = i / (D / 8), c = i % (D / 8) * 8;
         const uint4 v = *reinterpret_cast<const uint4 *>(staged + j * D + c);
-        if (row0 + j < rows)
+        if (row0 + j < rows && c < a.D)
           *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out_o) + out_at[j] + c) = v;
       }
     }
@@ -721,7 +732,8 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   if (tid == 0 && bars->gave_up && a.dev_status) atomicOr(a.dev_status, PSI_DEV_TIMEOUT);
 }
 
-// The pools as 4-dimensional tensors: element, slot, page, head.
+// The pools as 4-dimensional tensors: element, slot, page, head.  A box that
+// reaches past the head's last element is filled with zeros there.
 typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                 const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -792,7 +804,7 @@ cudaError_t launch_dim(const AttendArgs &a, const AttendPlan &p, cudaStream_t st
 }  // namespace
 
 bool attend_tc_fits(psi_dtype dtype, int32_t D) {
-  return dtype == PSI_DTYPE_BF16 && (D == 64 || D == 128);
+  return dtype == PSI_DTYPE_BF16 && D <= 128;
 }
 
 // Packed rows per CTA, in one group of up to 80 or two: as few CTAs as hold
@@ -811,7 +823,7 @@ cudaError_t launch_attend_tc(AttendArgs a, const AttendPlan &plan, cudaStream_t 
   const int64_t most = int64_t(1) << 39;  // (tensor maps take strides below 2^40 bytes)
   const bool tma = a.box >= 8 && encode_tiled() != nullptr && a.g.slot_stride < most &&
                    a.g.page_stride < most && a.g.head_stride < most;
-  if (a.D == 128)
+  if (a.D > 64)
     return tma ? launch_dim<128, true>(a, plan, stream) : launch_dim<128, false>(a, plan, stream);
   return tma ? launch_dim<64, true>(a, plan, stream) : launch_dim<64, false>(a, plan, stream);
 }

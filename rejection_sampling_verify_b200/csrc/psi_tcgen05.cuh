@@ -101,9 +101,8 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
 
 // ---- asynchronous copies ---------------------------------------------------------
 // 16 bytes, or 16 zeros where `there` is false (nothing is read then).
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16u : 0u)
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 // Arrive (one of the barrier's expected arrivals) once this thread's copies

@@ -119,6 +119,36 @@ def test_attend_long_lengths_are_split_and_joined(dtype):
         _check_attend(q, k, v, table, lens)
 
 
+@pytest.mark.parametrize("S", [16, 5])
+@pytest.mark.parametrize("D", [8, 40, 56, 72, 96, 120])
+def test_attend_heads_smaller_than_their_tile(D, S):
+    """bf16 heads that do not fill a tile's 64 or 128 elements, in pages that
+    are loaded as boxes and as single rows; what lies behind a head's last
+    element in memory is NaN and is neither read as keys nor as values."""
+    for seed, (N, R, Hq, H, lens) in enumerate([
+            (2, 1, 8, 2, [0, 300]), (2, 5, 6, 2, [127, 40]), (1, 33, 8, 2, [200]),
+            (2, 1, 4, 1, [4200, 9]), (1, 20, 8, 1, [2600])]):
+        g = 300 + 10 * D + seed
+        k, v, table, lens = _cache(N, lens, R, H, D, S, "bf16", g, heads_first=seed % 2 == 1)
+        q = torch.randn(N, R, Hq, D, generator=_gen(g)).bfloat16()
+        parents = _parents("tree", N, R, g)
+
+        def wide(t):  # the same values with 16 elements of NaN behind each head
+            w = torch.full((*t.shape[:-1], D + 16), math.nan, dtype=t.dtype, device="cuda")
+            w[..., :D] = t.cuda()
+            return w[..., :D]
+
+        r = psi.attend_block(wide(q), wide(k), wide(v), table.cuda(), lens.cuda(),
+                             parents=_cuda(parents), want_lse=True)
+        o, lse, tol = ref.attend(q, k, v, table, lens, parents)
+        assert bool(((r.o.cpu().double() - o).abs() <= tol).all())
+        assert torch.equal(torch.isfinite(r.lse.cpu()), torch.isfinite(lse))
+        assert int(r.status.item()) == 0
+        plain = psi.attend_block(q.cuda(), _cuda(k), _cuda(v), table.cuda(), lens.cuda(),
+                                 parents=_cuda(parents))
+        assert torch.equal(plain.o, r.o)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_attend_scores_far_apart(dtype):
     """Scores that rise by hundreds along the sequence, and fall: the running
