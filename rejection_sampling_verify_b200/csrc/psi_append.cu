@@ -275,17 +275,19 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendArgs a)
 
   if (position[mine] < 0) return;  // (the whole warp)
 
+  // (`half` is a multiple of 4: four pairs are turned together or not at all)
+  const bool turned[2] = {pair < half, pair + 4 < half};
   float c[8], s[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const bool turned = pair + k < half;
-    c[k] = turned ? cs[mine][pair + k] : 1.f;
-    s[k] = turned ? sn[mine][pair + k] : 0.f;
+    c[k] = turned[k / 4] ? cs[mine][pair + k] : 1.f;
+    s[k] = turned[k / 4] ? sn[mine][pair + k] : 0.f;
   }
   // One line of heads: norm, turn and store.
   const auto line = [&](const void *src, int64_t at, int64_t head_stride, int heads,
                         const void *weight, Bits *to, int64_t to_stride) {
-    // y1 = x1 w1 c - x2 w2 s, y2 = x2 w2 c + x1 w1 s, all over the root mean square
+    // y1 = x1 w1 c - x2 w2 s, y2 = x2 w2 c + x1 w1 s, all over the root mean
+    // square; y1 = x1 w1, y2 = x2 w2 where they are not turned
     float2 wc1[4], ws2[4], wc2[4], ws1[4];
     {
       float w1[8], w2[8];
@@ -329,9 +331,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendArgs a)
         for (int k = 0; k < 4; ++k) {
           const float2 u = make_float2(x1[2 * k] * inv, x1[2 * k + 1] * inv);
           const float2 v = make_float2(x2[2 * k] * inv, x2[2 * k + 1] * inv);
-          const float2 zero = make_float2(0.f, 0.f);
-          const float2 y1 = fma2(u, wc1[k], fma2(v, ws2[k], zero));
-          const float2 y2 = fma2(v, wc2[k], fma2(u, ws1[k], zero));
+          float2 y1 = mul2(u, wc1[k]), y2 = mul2(v, wc2[k]);
+          // (a factor of 0 does not take out a partner that is inf or NaN)
+          if (turned[k / 2]) {
+            y1 = fma2(v, ws2[k], y1);
+            y2 = fma2(u, ws1[k], y2);
+          }
           x1[2 * k] = y1.x;
           x1[2 * k + 1] = y1.y;
           x2[2 * k] = y2.x;
