@@ -85,8 +85,9 @@ typedef enum psi_dtype { PSI_DTYPE_F32 = 0, PSI_DTYPE_BF16 = 1 } psi_dtype;
                                    never expected; outputs are then invalid */
 #define PSI_DEV_BAD_PAGE 16u    /* cache: a position without a valid page (past
                                    the sequence's table, or a page index outside
-                                   the pool), or a page released more often than
-                                   it is held: that position is left out */
+                                   the pool), a page released more often than it
+                                   is held, or a stack entry that is no free
+                                   page: that position is left out */
 #define PSI_DEV_NO_PAGES 32u    /* cache: not enough free pages, or no room in
                                    the sequence's table: it got none */
 #define PSI_DEV_BAD_PATH 64u    /* cache: an accepted path that is not ascending
@@ -486,8 +487,10 @@ typedef struct psi_page_state {
  * are pushed on the free stack, lowest index first.  Then missing pages are
  * popped, in the order of (sequence, position); a sequence gets all that it
  * needs or none (and so do the later ones that need any, when the stack is
- * too low; a row too short for its sequence does not count).  lens[n] < 0:
- * left as it is.
+ * too low; a row too short for its sequence does not count).  A popped entry
+ * that is not a free page (out of range, held by a sequence, or popped before
+ * in the call) is flagged, and its place in the table becomes -1.
+ * lens[n] < 0: left as it is.
  * in and out may be the same state, or hold ten different arrays; table
  * entries beyond page_counts are not read.  Deterministic.
  * A forked sequence that is cut back to a length inside a page that it
@@ -508,7 +511,8 @@ size_t psi_cache_fork_workspace_bytes(int32_t K);
  * Whole pages are shared (refs rises by one); a page that the length ends
  * inside is copied, its filled slots in every layer, to a page popped from
  * the free stack (in the order of k; a fork gets its page or is left out,
- * and so are the later ones that need one).  out lens[dst] = lens[src].
+ * and so are the later ones that need one; an entry that is not a free page
+ * is flagged, and its fork left out).  out lens[dst] = lens[src].
  * A fork is left out and flagged when a row is out of [0, N), when dst holds
  * pages already, when dst is an earlier fork's dst, or any fork's src, or
  * when lens[src] < 0 or src lacks a page below its length.

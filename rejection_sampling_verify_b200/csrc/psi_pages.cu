@@ -130,6 +130,19 @@ __device__ int stack_height(const int32_t *n_free, int num_pages, uint32_t *dev_
   return n;
 }
 
+// A popped entry is a page only if nobody holds it, and only for the first
+// that pops it in this call.  Every pop claims its page by its place in the
+// order (the first one's claim is the lowest); after a barrier the claim that
+// stands takes it.  `at` is below `height`, the height of the stack.
+__device__ void claim_page(int32_t *refs, int32_t p, int num_pages, int at, int height) {
+  if (p >= 0 && p < num_pages && refs[p] <= 0) atomicMin(refs + p, at - height);
+}
+__device__ bool take_page(int32_t *refs, int32_t p, int num_pages, int at, int height) {
+  if (p < 0 || p >= num_pages || refs[p] != at - height) return false;
+  refs[p] = 1;
+  return true;
+}
+
 // A page whose last holder let it go in this call is marked until the stack
 // takes it: an erroneous second release of it then shows.
 constexpr int32_t kGone = -(1 << 30);
@@ -232,6 +245,7 @@ __global__ void __launch_bounds__(kPageThreads) resize_kernel(ResizeArgs a) {
     }
     const int64_t before = asked + block_scan(want, &sum);  // (and the pushes are done)
     asked += sum;
+    if (sum == 0) continue;  // (for all threads alike)
     const bool fits = before + want <= height;
     if (want && !fits) flag(PSI_DEV_NO_PAGES);
     first[tid] = fits ? (int32_t)before : 0;
@@ -240,16 +254,19 @@ __global__ void __launch_bounds__(kPageThreads) resize_kernel(ResizeArgs a) {
     if (fits && want) atomicMax(&given, (int)(before + want));
     __syncthreads();
     const int here = a.N - n0 < kPageThreads ? a.N - n0 : kPageThreads;
+    for (int i = tid / 32; i < here; i += kPageThreads / 32)
+      for (int j = lane; j < count[i]; j += 32)
+        claim_page(refs, a.out.free_pages[height - 1 - (first[i] + j)], a.num_pages, first[i] + j,
+                   height);
+    __syncthreads();
     for (int i = tid / 32; i < here; i += kPageThreads / 32) {
       if (!count[i]) continue;
       int32_t *row = a.out.page_table + (int64_t)(n0 + i) * a.max_pages + base[i];
       for (int j = lane; j < count[i]; j += 32) {
-        int32_t p = a.out.free_pages[height - 1 - (first[i] + j)];
-        if (p < 0 || p >= a.num_pages || atomicExch(refs + p, 1) != 0) {
-          flag(PSI_DEV_BAD_PAGE);  // not a free page
-          if (p < 0 || p >= a.num_pages) p = -1;
-        }
-        row[j] = p;
+        const int at = first[i] + j, p = a.out.free_pages[height - 1 - at];
+        const bool mine = take_page(refs, p, a.num_pages, at, height);
+        if (!mine) flag(PSI_DEV_BAD_PAGE);
+        row[j] = mine ? p : -1;
       }
       if (lane == 0) a.out.page_counts[n0 + i] = base[i] + count[i];
     }
@@ -312,16 +329,15 @@ __global__ void __launch_bounds__(kPageThreads) fork_kernel(ForkArgs a) {
     int64_t sum;
     const int64_t at = asked + block_scan(needs, &sum);
     asked += sum;
-    int32_t p = -1;
+    const bool there = needs && at < height;
+    const int32_t p = there ? a.out.free_pages[height - 1 - at] : -1;
+    if (there) claim_page(a.out.refs, p, a.num_pages, (int)at, height);
+    __syncthreads();
     if (needs) {
-      if (at < height) p = a.out.free_pages[height - 1 - at];
-      if (at >= height) flag(PSI_DEV_NO_PAGES);
-      else if (p < 0 || p >= a.num_pages || atomicExch(a.out.refs + p, 1) != 0) {
-        flag(PSI_DEV_BAD_PAGE);
-        p = -1;
-      }
-      a.copies[k].to = p;
-      if (p < 0) a.copies[k].count = -1;
+      const bool mine = there && take_page(a.out.refs, p, a.num_pages, (int)at, height);
+      if (!mine) flag(there ? PSI_DEV_BAD_PAGE : PSI_DEV_NO_PAGES);
+      a.copies[k].to = mine ? p : -1;
+      if (!mine) a.copies[k].count = -1;
     }
   }
   given = asked < height ? asked : height;
