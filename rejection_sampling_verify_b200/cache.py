@@ -13,10 +13,13 @@ them on the current stream.  The order of a serving step is
                    verify the new length is lens + n_emitted
     cache_resize   pages behind the new length go back
     cache_fork     a sequence is continued more than once
+
+With ``stream`` a call is made as under ``torch.cuda.stream(stream)``: outputs
+and workspace are that stream's memory too.  The inputs' memory is the
+caller's to keep, and its order with that stream the caller's to see to.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import math
 import os
@@ -288,24 +291,15 @@ _status_words = {}
 
 
 def _new_status(dev: int, stream: int):
-    """A zeroed status word for a call on `stream` (a raw handle) of `dev`."""
+    """A zeroed status word for a call on the current stream (a raw handle) of `dev`."""
     torch = _torch()
-    if torch.cuda.is_current_stream_capturing() or \
-            stream != torch._C._cuda_getCurrentRawStream(dev):
-        # (zeroed by the graph on every replay; or on the stream that the call names)
-        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=dev)) \
-                if stream != torch._C._cuda_getCurrentRawStream(dev) \
-                else contextlib.nullcontext():
-            return torch.zeros(1, dtype=torch.int32, device=dev)
+    if torch.cuda.is_current_stream_capturing():  # (zeroed by the graph on every replay)
+        return torch.zeros(1, dtype=torch.int32, device=dev)
     words = _status_words.get((dev, stream))
     if not words:
         words = list(torch.zeros(_STATUS_WORDS, dtype=torch.int32, device=dev).split(1))
         _status_words[dev, stream] = words
     return words.pop()
-
-
-def _raw_stream(stream, dev: int) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def rope_frequencies(rotary_dim: int, theta: float = 1e6, factor: float = 1.0,
@@ -357,7 +351,11 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight=None, k_w
     inv_freq float64 [rotary_dim / 2] or None; parents int32 [N, R - 1] or
     None (a chain).  ``out.q`` may be ``q`` itself.
     """
-    if out is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return cache_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight, k_weight,
+                                eps, inv_freq, interleaved, rope_scale, parents, out=out)
+    if out is None:
         r = (_binding or _short()).append(q, k, v, k_pages, v_pages, page_table, lens, q_weight,
                                           k_weight, eps, inv_freq, interleaved, rope_scale,
                                           parents)
@@ -377,7 +375,7 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight=None, k_w
         _check_out("status", out.status, torch.int32, (1,))
         others.update(out_q=out.q, status=out.status)
     dev = _on_device(q, others)
-    raw = _raw_stream(stream, dev)
+    raw = _torch()._C._cuda_getCurrentRawStream(dev)
     if out is None:
         out = AppendResult(_torch().empty(q.shape, dtype=q.dtype, device=q.device),
                            _new_status(dev, raw))
@@ -421,7 +419,11 @@ def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: flo
     D ** -0.5.  With ``out`` and a large enough ``workspace`` the call only
     launches work on the stream.
     """
-    if out is None and workspace is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return attend_block(q, k_pages, v_pages, page_table, lens, parents, scale, want_lse,
+                                workspace, out=out)
+    if out is None and workspace is None:
         r = (_binding or _short()).attend(q, k_pages, v_pages, page_table, lens, parents, scale,
                                           want_lse)
         if r is not None:
@@ -442,7 +444,7 @@ def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: flo
         others.update(o=out.o, lse=out.lse, status=out.status)
     _check_workspace(workspace)
     dev = _on_device(q, others)
-    raw = _raw_stream(stream, dev)
+    raw = _torch()._C._cuda_getCurrentRawStream(dev)
     device = q.device
     if out is None:
         out = AttendResult(torch.empty(q.shape, dtype=q.dtype, device=device),
@@ -478,7 +480,10 @@ def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, strea
     int32 [N] as :func:`verify_tree_greedy` and :func:`verify_tree_sampled`
     return them.  Returns the new lengths (``out.lens`` is not ``lens``).
     """
-    if out is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, out=out)
+    if out is None:
         r = (_binding or _short()).commit(k_pages, v_pages, page_table, lens, path_nodes,
                                           path_len)
         if r is not None:
@@ -497,7 +502,7 @@ def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, strea
         _check_out("status", out.status, torch.int32, (1,))
         others.update(out_lens=out.lens, status=out.status)
     dev = _on_device(k_pages, others)
-    raw = _raw_stream(stream, dev)
+    raw = _torch()._C._cuda_getCurrentRawStream(dev)
     if out is None:
         out = CommitResult(torch.empty_like(lens), _new_status(dev, raw))
     st = psi_cache_commit(lay, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
@@ -554,7 +559,10 @@ def cache_resize(pages: PageState, lens, extra: int, page_size: int, stream=None
     """Fit each sequence's pages to lens[n] + extra positions
     (``psi_cache_resize``).  Returns a new state; with ``out.pages = pages``
     the state is changed in place."""
-    if out is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return cache_resize(pages, lens, extra, page_size, out=out)
+    if out is None:
         r = (_binding or _short()).resize(pages.table, pages.counts, pages.refs, pages.free,
                                           pages.n_free, lens, extra, page_size)
         if r is not None:
@@ -568,7 +576,7 @@ def cache_resize(pages: PageState, lens, extra: int, page_size: int, stream=None
         _check_out("status", out.status, _torch().int32, (1,))
         others.update(_named("out.pages", out.pages), status=out.status)
     dev = _on_device(pages.table, others)
-    raw = _raw_stream(stream, dev)
+    raw = _torch()._C._cuda_getCurrentRawStream(dev)
     if out is None:
         out = ResizeResult(_like(pages, N, max_pages, P), _new_status(dev, raw))
     st = psi_cache_resize(N, max_pages, P, page_size, lens.data_ptr(), extra, _state_ptrs(pages),
@@ -595,7 +603,10 @@ def cache_fork(k_pages, v_pages, pages: PageState, lens, src, dst, workspace=Non
     k_pages, v_pages [L, P, S, H, D]; src, dst int32 [K].  Returns a new
     state and lengths; ``out`` may name the given ones (in place).
     """
-    if out is None and workspace is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return cache_fork(k_pages, v_pages, pages, lens, src, dst, workspace, out=out)
+    if out is None and workspace is None:
         r = (_binding or _short()).fork(k_pages, v_pages, pages.table, pages.counts, pages.refs,
                                         pages.free, pages.n_free, lens, src, dst)
         if r is not None:
@@ -615,7 +626,7 @@ def cache_fork(k_pages, v_pages, pages: PageState, lens, src, dst, workspace=Non
         others.update(_named("out.pages", out.pages), out_lens=out.lens, status=out.status)
     _check_workspace(workspace)
     dev = _on_device(k_pages, others)
-    raw = _raw_stream(stream, dev)
+    raw = _torch()._C._cuda_getCurrentRawStream(dev)
     if out is None:
         out = ForkResult(_like(pages, N, max_pages, P), torch.empty_like(lens),
                          _new_status(dev, raw))

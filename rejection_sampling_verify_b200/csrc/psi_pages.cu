@@ -370,7 +370,10 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(ForkArgs a) {
   pdl_wait();
   pdl_trigger();
   const PageCopy c = a.copies[blockIdx.x];
-  if (c.count <= 0) return;
+  // (the bookkeeping leaves nothing else; memory that a caller let go of may hold anything)
+  if (c.count <= 0 || c.count > a.page_size || c.from < 0 || c.from >= a.num_pages || c.to < 0 ||
+      c.to >= a.num_pages)
+    return;
   char *base = static_cast<char *>(blockIdx.z ? a.v_pool : a.k_pool) + blockIdx.y * a.layer_bytes;
   const int per_slot = a.kv_heads * a.head_vecs;
   for (int i = threadIdx.x; i < c.count * per_slot; i += kCopyThreads) {
