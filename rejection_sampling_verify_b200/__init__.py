@@ -6,8 +6,10 @@ arguments: the raw functions below carry the ABI's names and arguments
 one-for-one (device pointers as integers), and the tensor helpers
 (:func:`verify_linear`, :func:`verify_tree_greedy`, :func:`rng_uniforms`, and
 the key-value cache's :func:`cache_append`, :func:`attend_block`,
-:func:`cache_commit`, :func:`cache_resize` and :func:`cache_fork`) take ``torch`` CUDA tensors, allocate outputs and workspace with torch, and
-call the raw functions on the current stream.
+:func:`cache_commit`, :func:`cache_resize` and :func:`cache_fork`) take
+``torch`` CUDA tensors, allocate outputs and workspace with torch, and call
+the raw functions on the current stream.  With ``stream`` a helper is called
+as under ``torch.cuda.stream(stream)``: what it allocates is that stream's.
 
 There is no fallback: if the library is missing or cannot load, every call
 raises.
@@ -307,10 +309,8 @@ def _device_of(ref, **tensors):
     return dev
 
 
-def _stream(stream):
-    torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+def _stream():
+    return _torch().cuda.current_stream().cuda_stream
 
 
 def _check(status, where):
@@ -342,6 +342,10 @@ def verify_linear(ar, draft, ids, temperature: float, top_p: float = 1.0, seed: 
     fixed in the graph.
     """
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_linear(ar, draft, ids, temperature, top_p, seed, step, seq_ids,
+                                 want_probs, workspace, out=out, top_k=top_k)
     N, B1 = ar.shape[0], ar.shape[1]
     B = B1 - 1
     ar_stride, V = _rows(ar, 2, "ar")
@@ -386,7 +390,7 @@ def verify_linear(ar, draft, ids, temperature: float, top_p: float = 1.0, seed: 
             B, V, float(temperature), float(top_p), int(top_k), int(seed) & (2**64 - 1),
             _ptr(seq_ids), int(step) & (2**64 - 1), _ptr(out.tokens), _ptr(out.n_emitted),
             _ptr(out.p_draft), _ptr(out.q_draft), _ptr(out.status), _ptr(workspace),
-            _nbytes(workspace), _stream(stream))
+            _nbytes(workspace), _stream())
         _check(st, "psi_verify_linear_topk")
         return out
     st = psi_verify_linear(
@@ -394,7 +398,7 @@ def verify_linear(ar, draft, ids, temperature: float, top_p: float = 1.0, seed: 
         V, float(temperature), float(top_p), int(seed) & (2**64 - 1),
         _ptr(seq_ids), int(step) & (2**64 - 1), _ptr(out.tokens), _ptr(out.n_emitted),
         _ptr(out.p_draft), _ptr(out.q_draft), _ptr(out.status), _ptr(workspace),
-        _nbytes(workspace), _stream(stream))
+        _nbytes(workspace), _stream())
     _check(st, "psi_verify_linear")
     return out
 
@@ -411,6 +415,9 @@ def verify_tree_greedy(ar, node_tokens, parents, workspace=None, stream=None,
                        out: TreeResult | None = None) -> TreeResult:
     """Greedy tree verify.  ar [N, M+1, V]; node_tokens, parents int32 [N, M]."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_tree_greedy(ar, node_tokens, parents, workspace, out=out)
     N, M1 = ar.shape[0], ar.shape[1]
     M = M1 - 1
     stride, V = _rows(ar, 2, "ar")
@@ -441,7 +448,7 @@ def verify_tree_greedy(ar, node_tokens, parents, workspace=None, stream=None,
     st = psi_verify_tree_greedy(_ptr(ar), stride, code, _ptr(node_tokens), _ptr(parents), N, M,
                                 V, _ptr(out.path_nodes), _ptr(out.path_len), _ptr(out.tokens),
                                 _ptr(out.status), _ptr(workspace),
-                                _nbytes(workspace), _stream(stream))
+                                _nbytes(workspace), _stream())
     _check(st, "psi_verify_tree_greedy")
     return out
 
@@ -453,6 +460,10 @@ def verify_tree_sampled(ar, node_tokens, parents, temperature: float, top_p: flo
     children).  ar [N, M+1, V]; node_tokens, parents int32 [N, M]; seq_ids
     int64 [N] (read as uint64) or None."""
     torch = _torch()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return verify_tree_sampled(ar, node_tokens, parents, temperature, top_p, seed, step,
+                                       seq_ids, workspace, out=out)
     N, M1 = ar.shape[0], ar.shape[1]
     M = M1 - 1
     stride, V = _rows(ar, 2, "ar")
@@ -488,7 +499,7 @@ def verify_tree_sampled(ar, node_tokens, parents, temperature: float, top_p: flo
                                  V, float(temperature), float(top_p), int(seed) & (2**64 - 1),
                                  _ptr(seq_ids), int(step) & (2**64 - 1), _ptr(out.path_nodes),
                                  _ptr(out.path_len), _ptr(out.tokens), _ptr(out.status),
-                                 _ptr(workspace), _nbytes(workspace), _stream(stream))
+                                 _ptr(workspace), _nbytes(workspace), _stream())
     _check(st, "psi_verify_tree_sampled")
     return out
 
@@ -499,11 +510,14 @@ def rng_uniforms(seed: int, n_seq: int, step: int, n_rows: int, purpose: int, se
     torch = _torch()
     if torch.device(device).type != "cuda":
         raise ValueError(f"device must be a CUDA device (got {device}): the library has no CPU path")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return rng_uniforms(seed, n_seq, step, n_rows, purpose, seq_ids, device)
     _check_seq_ids(seq_ids, n_seq)
     out = torch.empty(n_seq, n_rows, dtype=torch.float32, device=device)
     _device_of(out, seq_ids=seq_ids)
     st = psi_rng_uniforms(int(seed) & (2**64 - 1), _ptr(seq_ids), n_seq, int(step) & (2**64 - 1),
-                          n_rows, purpose, _ptr(out), _stream(stream))
+                          n_rows, purpose, _ptr(out), _stream())
     _check(st, "psi_rng_uniforms")
     return out
 

@@ -78,3 +78,26 @@ def test_pages_on_a_busy_stream():
             assert torch.equal(getattr(a.pages, f), getattr(b.pages, f)), f
         assert int(a.status.item()) == 0
     assert torch.equal(r.lens, want[2].lens)
+
+
+def test_verify_on_a_busy_stream():
+    N, B, V = 3, 4, 1000
+    g = torch.Generator().manual_seed(3)
+    ar = torch.randn(N, B + 1, V, generator=g).cuda()
+    draft = torch.randn(N, B, V, generator=g).cuda()
+    ids = torch.randint(0, V, (N, B), generator=g, dtype=torch.int32).cuda()
+    parents = torch.tensor([[-1, 0, -1, 2]] * N, dtype=torch.int32).cuda()
+    calls = [lambda s: psi.verify_linear(ar, draft, ids, 0.8, 0.9, seed=5, stream=s),
+             lambda s: psi.verify_linear(ar, draft, ids, 0.8, seed=5, top_k=20, stream=s),
+             lambda s: psi.verify_linear(ar, None, ids, 0.0, stream=s),
+             lambda s: psi.verify_tree_greedy(ar, ids, parents, stream=s),
+             lambda s: psi.verify_tree_sampled(ar, ids, parents, 0.8, seed=6, stream=s)]
+    s = torch.cuda.Stream()
+    for call in calls:
+        want, got = call(None), _behind(s, call)
+        for name, t in vars(want).items():
+            if t is not None:
+                assert torch.equal(getattr(got, name), t), name
+    u = psi.rng_uniforms(7, N, 1, B, psi.PSI_PURPOSE_ACCEPT)
+    got = _behind(s, lambda s: psi.rng_uniforms(7, N, 1, B, psi.PSI_PURPOSE_ACCEPT, stream=s))
+    assert torch.equal(got, u)

@@ -77,7 +77,7 @@ def _inputs():
         lens=torch.ones(N).to(i32), path=torch.ones(N, M).to(i32), src=torch.ones(1).to(i32),
         pages=psi.PageState(torch.ones(N, 4).to(i32), torch.ones(N).to(i32), torch.ones(P).to(i32),
                             torch.ones(P).to(i32), torch.ones(1).to(i32)),
-        logits=torch.ones(N, M + 1, V))
+        logits=torch.ones(N, M + 1, V), draft=torch.ones(N, M, V))
 
 
 CALLS = {
@@ -96,6 +96,17 @@ CALLS = {
     "fork_out": lambda t, s: psi.cache_fork(
         t["pool"], t["pool"], t["pages"], t["lens"], t["src"], t["src"], stream=s,
         out=psi.ForkResult(t["pages"], t["lens"], t["src"].clone())),
+    "linear": lambda t, s: psi.verify_linear(t["logits"], t["draft"], t["path"], 0.7, stream=s),
+    "linear_topk": lambda t, s: psi.verify_linear(t["logits"], t["draft"], t["path"], 0.7,
+                                                  want_probs=False, top_k=3, stream=s),
+    "linear_out": lambda t, s: psi.verify_linear(
+        t["logits"], None, t["path"], 0.0, stream=s,
+        out=psi.LinearResult(t["path"].new_ones(N, M + 1), t["lens"].clone(), None, None,
+                             t["src"].clone())),
+    "tree_greedy": lambda t, s: psi.verify_tree_greedy(t["logits"], t["path"], t["path"], stream=s),
+    "tree_sampled": lambda t, s: psi.verify_tree_sampled(t["logits"], t["path"], t["path"], 0.7,
+                                                         stream=s),
+    "uniforms": lambda t, s: psi.rng_uniforms(1, N, 2, 3, psi.PSI_PURPOSE_ACCEPT, stream=s),
 }
 
 
