@@ -11,6 +11,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
@@ -121,17 +122,26 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType dtype, int device) {
 }
 
 // Status words, zeroed many at a time on the stream that uses them; each is
-// handed out once.  A call that is being captured gets one that its graph
-// zeroes on every replay.
+// handed out once, to a later call on that stream.  Two kinds of call get one
+// of their own: one that is being captured (its graph zeroes it on every
+// replay), and one on a stream that is not torch's, whose handle may be
+// another stream's by the next call.
 Tensor new_status(const Call &c) {
   const auto zeros = [&](int64_t n) {
     return at::zeros({n}, at::TensorOptions().dtype(at::kInt).device(at::kCUDA, c.device));
   };
-  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
+  // (a stream from outside is known by its handle)
+  const c10::cuda::CUDAStream s = c10::cuda::getCurrentCUDAStream(c.device);
+  const bool outside = s.id() != 0 && s.id() == reinterpret_cast<int64_t>(s.stream());
+  if (outside || c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None)
     return zeros(1);
   static auto *words = new std::map<std::pair<int, void *>, std::vector<Tensor>>;
-  std::vector<Tensor> &w = (*words)[{c.device, (void *)c.stream()}];
-  if (w.empty()) w = zeros(256).split(1);
+  std::vector<Tensor> &w = (*words)[{c.device, (void *)s.stream()}];
+  if (w.empty()) {
+    // later calls may be made outside the inference mode that this one is in
+    c10::InferenceMode normal(false);
+    w = zeros(256).split(1);
+  }
   Tensor t = std::move(w.back());
   w.pop_back();
   return t;

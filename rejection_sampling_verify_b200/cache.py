@@ -285,21 +285,8 @@ def _on_device(ref, named):
     return dev
 
 
-# Status words, zeroed many at a time: each is handed out once.
-_STATUS_WORDS = 256
-_status_words = {}
-
-
-def _new_status(dev: int, stream: int):
-    """A zeroed status word for a call on the current stream (a raw handle) of `dev`."""
-    torch = _torch()
-    if torch.cuda.is_current_stream_capturing():  # (zeroed by the graph on every replay)
-        return torch.zeros(1, dtype=torch.int32, device=dev)
-    words = _status_words.get((dev, stream))
-    if not words:
-        words = list(torch.zeros(_STATUS_WORDS, dtype=torch.int32, device=dev).split(1))
-        _status_words[dev, stream] = words
-    return words.pop()
+def _new_status(dev: int):
+    return _torch().zeros(1, dtype=_torch().int32, device=dev)
 
 
 def rope_frequencies(rotary_dim: int, theta: float = 1e6, factor: float = 1.0,
@@ -378,7 +365,7 @@ def cache_append(q, k, v, k_pages, v_pages, page_table, lens, q_weight=None, k_w
     raw = _torch()._C._cuda_getCurrentRawStream(dev)
     if out is None:
         out = AppendResult(_torch().empty(q.shape, dtype=q.dtype, device=q.device),
-                           _new_status(dev, raw))
+                           _new_status(dev))
     st = psi_cache_append(
         lay, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), max_pages,
         lens.data_ptr(), N, R, Hq, q.data_ptr(), *strides[0], k.data_ptr(), *strides[1],
@@ -449,7 +436,7 @@ def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: flo
     if out is None:
         out = AttendResult(torch.empty(q.shape, dtype=q.dtype, device=device),
                            torch.empty(q.shape[:3], dtype=torch.float32, device=device)
-                           if want_lse else None, _new_status(dev, raw))
+                           if want_lse else None, _new_status(dev))
     if workspace is None or _nbytes(workspace) < ws_bytes:
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
     st = psi_attend_block(lay, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
@@ -504,7 +491,7 @@ def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, strea
     dev = _on_device(k_pages, others)
     raw = _torch()._C._cuda_getCurrentRawStream(dev)
     if out is None:
-        out = CommitResult(torch.empty_like(lens), _new_status(dev, raw))
+        out = CommitResult(torch.empty_like(lens), _new_status(dev))
     st = psi_cache_commit(lay, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
                           max_pages, lens.data_ptr(), N, M, path_nodes.data_ptr(),
                           path_len.data_ptr(), out.lens.data_ptr(), out.status.data_ptr(), raw)
@@ -578,7 +565,7 @@ def cache_resize(pages: PageState, lens, extra: int, page_size: int, stream=None
     dev = _on_device(pages.table, others)
     raw = _torch()._C._cuda_getCurrentRawStream(dev)
     if out is None:
-        out = ResizeResult(_like(pages, N, max_pages, P), _new_status(dev, raw))
+        out = ResizeResult(_like(pages, N, max_pages, P), _new_status(dev))
     st = psi_cache_resize(N, max_pages, P, page_size, lens.data_ptr(), extra, _state_ptrs(pages),
                           _state_ptrs(out.pages), out.status.data_ptr(), raw)
     _check(st, "psi_cache_resize")
@@ -629,7 +616,7 @@ def cache_fork(k_pages, v_pages, pages: PageState, lens, src, dst, workspace=Non
     raw = _torch()._C._cuda_getCurrentRawStream(dev)
     if out is None:
         out = ForkResult(_like(pages, N, max_pages, P), torch.empty_like(lens),
-                         _new_status(dev, raw))
+                         _new_status(dev))
     if workspace is None or _nbytes(workspace) < ws_bytes:
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=k_pages.device)
     st = psi_cache_fork(lay, k_pages.data_ptr(), v_pages.data_ptr(), N, max_pages,

@@ -44,3 +44,18 @@ def test_status_words_are_not_shared():
     words = [_resize().status for _ in range(600)]
     assert len({w.data_ptr() for w in words}) == 600
     assert not any(int(w) for w in torch.cat(words).tolist())
+
+
+def test_status_words_of_captured_calls_are_zeroed_on_every_replay():
+    pages = psi.PageState.empty(2, 4, 8)
+    lens = torch.tensor([20, 3], dtype=torch.int32, device="cuda")
+    psi.cache_resize(pages, lens, 1, 16)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = psi.cache_resize(pages, lens, 1, 16)
+    lens[0] = 1000  # more than a row holds
+    g.replay()
+    assert int(r.status.item()) == psi.PSI_DEV_NO_PAGES
+    lens[0] = 20
+    g.replay()
+    assert int(r.status.item()) == 0
