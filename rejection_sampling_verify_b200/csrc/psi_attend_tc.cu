@@ -27,6 +27,10 @@
 // three on an otherwise idle device; for the batch below gathers took 301 us
 // where the boxes took 232).
 //
+// Accesses to tensor memory and changes of register counts are the whole
+// warp's (.sync.aligned): a __syncwarp() stands between each and what may
+// have parted the lanes before it.
+//
 // Warps: four of softmax for each group of NT rows; one each that loads keys,
 // loads values, issues the products K Q^T and issues V^T P^T.  Keys and
 // values have stages of their own, so that the next keys load while the
@@ -324,6 +328,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     tmem_alloc(&bars->tmem, T::kCols);
   }
   __syncthreads();
+  __syncwarp();
   const uint32_t tmem = bars->tmem;
   volatile uint32_t *gave_up = &bars->gave_up;
 
@@ -565,15 +570,18 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
                 *reinterpret_cast<float4 *>(nrefs + c + j) =
                     make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
             }
+            __syncwarp();
           }
         }
         named_sync(sync, kSoft);
+        __syncwarp();
       }
       if (!raise) {
         const float all = masked ? weigh_tile(true_type{}, false_type{})
                                  : weigh_tile(false_type{}, false_type{});
         if (kGroups == 2 && !(g == 1 && i == tiles - 1)) named_arrive(kTurn + 1 - g, 2 * kSoft);
         raise = named_or(sync, kSoft, !(all <= kFar));
+        __syncwarp();
       } else if (kGroups == 2 && !(g == 1 && i == tiles - 1)) {
         named_arrive(kTurn + 1 - g, 2 * kSoft);
       }
@@ -590,6 +598,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
           for (int j = 0; j < 16; ++j) s[j] = (sees >> j) & 1u ? s[j] * a.scale2 : kMinusInf;
           const float m = reduce16(s, [](float x, float y) { return fmaxf(x, y); });
           if (lane < 16) wred[warp % 4 * NT + c + lane] = m;
+          __syncwarp();
         }
         named_sync(sync, kSoft);
         if (st < NT) {
@@ -603,6 +612,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
         }
         if (i > 0) wait_or_give_up(&bar.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
         named_sync(sync, kSoft);
+        __syncwarp();
         tc_fence_after();
         if (i > 0) {
 #pragma unroll 1
@@ -676,41 +686,43 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       float *o = ahead[c / 16 % 2];
       tmem_wait_ld16(o);
       if (c + 16 < NT) tmem_ld16(own + 2 * NT + c + 16, ahead[1 - c / 16 % 2]);
-      if (d >= a.D) continue;
-      if (fix) {
-        for (int x = 0; x < a.R; ++x) {
-          if (!((bars->fix_tokens[x / 32] >> (x % 32)) & 1u)) continue;
-          const int64_t off = slot_offset(a.g, table, (int64_t)len + x);
-          if (off < 0) continue;  // (what lay in place of a bad page was seen by nobody)
-          const uint16_t v =
-              static_cast<const uint16_t *>(a.v)[off + (int64_t)h * a.g.head_stride + d];
-          // (times its weight it is what it is)
-          if (!not_finite(v)) continue;
-          const uint32_t seers = desc[x * T::kMaskWords + c / 32] >> (c % 32);
+      if (d < a.D) {
+        if (fix) {
+          for (int x = 0; x < a.R; ++x) {
+            if (!((bars->fix_tokens[x / 32] >> (x % 32)) & 1u)) continue;
+            const int64_t off = slot_offset(a.g, table, (int64_t)len + x);
+            if (off < 0) continue;  // (what lay in place of a bad page was seen by nobody)
+            const uint16_t v =
+                static_cast<const uint16_t *>(a.v)[off + (int64_t)h * a.g.head_stride + d];
+            // (times its weight it is what it is)
+            if (!not_finite(v)) continue;
+            const uint32_t seers = desc[x * T::kMaskWords + c / 32] >> (c % 32);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if ((seers >> j) & 1u) o[j] += Elem<uint16_t>::to_float(v);
+          }
+        }
+        float f[16];
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<float4 *>(f + j) = *reinterpret_cast<const float4 *>(facs + c + j);
+        if (!joined) {
+          uint16_t b[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)  // (a row that sees nothing: 0 whatever the others saw)
+            b[j] = __bfloat16_as_ushort(__float2bfloat16(f[j] == 0.f ? 0.f : o[j] * f[j]));
+#pragma unroll
+          for (int j = 0; j < 16; ++j) staged[(c + j) * D + d] = b[j];
+        } else {
+          int64_t at[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) at[j] = out_at[c + j] + d;
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if ((seers >> j) & 1u) o[j] += Elem<uint16_t>::to_float(v);
+            if (row0 + c + j < rows) a.part_o[at[j]] = o[j];
         }
       }
-      float f[16];
-#pragma unroll
-      for (int j = 0; j < 16; j += 4)
-        *reinterpret_cast<float4 *>(f + j) = *reinterpret_cast<const float4 *>(facs + c + j);
-      if (!joined) {
-        uint16_t b[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j)  // (a row that sees nothing: 0 whatever the others saw)
-          b[j] = __bfloat16_as_ushort(__float2bfloat16(f[j] == 0.f ? 0.f : o[j] * f[j]));
-#pragma unroll
-        for (int j = 0; j < 16; ++j) staged[(c + j) * D + d] = b[j];
-      } else {
-        int64_t at[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) at[j] = out_at[c + j] + d;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (row0 + c + j < rows) a.part_o[at[j]] = o[j];
-      }
+      __syncwarp();  // (heads end inside a warp)
     }
     if (!joined) {
       named_sync(sync, kSoft);
@@ -724,6 +736,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     }
     tc_fence_before();
   }
+  __syncwarp();
   __syncthreads();
   if (warp == kLoadWarp + 2) {
     tc_fence_after();
