@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   uint64_t *full = keys ? bars->k_full : bars->v_full, *free = keys ? bars->k_free : bars->v_free;
   uint8_t *ring = keys ? kring : vring;
   Loader<D, kTma> loader;
+  int issued = tiles < stages ? tiles : stages;  // tiles whose loads are on their way or done
   if (loads) {
     if (lane == 0) {
       for (int s = 0; s < 3; ++s) {
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     loader.end = end;
     loader.h = h;
     loader.start(a, lane);
-    for (int i = 0; i < stages && i < tiles; ++i) loader.load(a, i, i, lane);
+    for (int i = 0; i < issued; ++i) loader.load(a, i, i, lane);
   } else if (warp == kLoadWarp + 2) {
     if (lane == 0) {
       for (int b = 0; b < 2; ++b) {
@@ -335,12 +336,12 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   if (tiles > 0 && warp >= kLoadWarp) {
     shrink_registers<T::kLoadRegs>();
     if (loads) {
-      for (int i = stages; i < tiles; ++i) {
-        const int slot = i % stages;
+      for (; issued < tiles; ++issued) {
+        const int slot = issued % stages;
         // the stage is free once the products that read it are done
-        const bool ok = wait_or_give_up(&free[slot], (i / stages - 1) & 1, gave_up);
+        const bool ok = wait_or_give_up(&free[slot], (issued / stages - 1) & 1, gave_up);
         if (!__all_sync(0xFFFFFFFFu, ok)) break;
-        loader.load(a, i, slot, lane);
+        loader.load(a, issued, slot, lane);
       }
       if (!kTma) copy_wait_all();
     } else {
@@ -742,7 +743,14 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     tc_fence_after();
     tmem_free(tmem, T::kCols);
   }
-  if (tid == 0 && bars->gave_up && a.dev_status) atomicOr(a.dev_status, PSI_DEV_TIMEOUT);
+  if (bars->gave_up) {
+    // nobody may have waited for the last boxes: none lands in shared memory
+    // that is another CTA's by then
+    if (kTma && loads && lane == 0)
+      for (int i = issued < stages ? 0 : issued - stages; i < issued; ++i)
+        mbar_wait_bounded(&full[i % stages], (i / stages) & 1);
+    if (tid == 0 && a.dev_status) atomicOr(a.dev_status, PSI_DEV_TIMEOUT);
+  }
 }
 
 // The pools as 4-dimensional tensors: element, slot, page, head.  A box that
