@@ -49,10 +49,6 @@ __device__ __forceinline__ void unpack(const Raw8<Bits> &r, bool there, float f[
                  : 0.f;
 }
 template <typename Bits>
-__device__ __forceinline__ void load8(const void *base, int64_t at, float f[8]) {
-  unpack<Bits>(load_raw<Bits>(base, at), true, f);
-}
-template <typename Bits>
 __device__ __forceinline__ Raw8<Bits> pack(const float f[8]) {
   Raw8<Bits> r;
   if constexpr (sizeof(Bits) == 2) {
