@@ -37,8 +37,8 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kernel(CommitArgs a, in
   __syncthreads();
   bool bad = false;
   if (tid < count) {  // the path is kept up to its first node that does not ascend within [0, M)
-    const int node = nodes[tid], before = tid ? nodes[tid - 1] : -1;
-    if (node <= before || node >= a.M) {
+    const int node = nodes[tid];
+    if (path_prefix(nodes, count, a.M, tid, kCommitThreads) < count) {
       atomicMin(&kept, tid);
     } else {
       const auto place = [&](int64_t t) {

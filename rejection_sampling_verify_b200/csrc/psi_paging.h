@@ -75,20 +75,20 @@ PSI_HD bool row_sees(const int32_t *parents, int32_t r, uint32_t bits[kBlockWord
 }
 
 // Nodes of an accepted path that can be kept: the leading entries that ascend
-// within [0, M).
-PSI_HD int32_t path_prefix(const int32_t *nodes, int32_t len, int32_t M) {
-  int32_t n = len < 0 ? 0 : len > M ? M : len;
-  int32_t last = -1;
-  for (int32_t j = 0; j < n; ++j) {
-    if (nodes[j] <= last || nodes[j] >= M) return j;
-    last = nodes[j];
-  }
+// within [0, M).  With `step` over 1 only entries first, first + step, ... are
+// looked at; the minimum over first = 0..step - 1 is the answer.
+PSI_HD int32_t path_prefix(const int32_t *nodes, int32_t len, int32_t M, int32_t first = 0,
+                           int32_t step = 1) {
+  const int32_t n = len < 0 ? 0 : len > M ? M : len;
+  for (int32_t j = first; j < n; j += step)
+    if (nodes[j] <= (j ? nodes[j - 1] : -1) || nodes[j] >= M) return j;
   return n;
 }
 
 // How a sequence's positions are dealt to the CTAs of its rows: `units`
-// ranges of `per` positions (a multiple of the tile), at most `splits` of
-// them and none below `least` tiles.
+// ranges of `per` positions (a multiple of the tile), alike but for a shorter
+// last one and never empty; at most `splits` of them, and no more than ranges
+// of `least` tiles would make.
 struct Ranges {
   int32_t units, per;
 };
