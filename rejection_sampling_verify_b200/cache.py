@@ -254,8 +254,8 @@ def _short():
 
 
 # A call's shapes, strides and dtypes decide what it may do: they are checked
-# once, and what was found (the layout, the strides, the workspace's size) is
-# kept under them.
+# once, and what was found (the layout, the strides) is kept under them; the
+# attention's workspace also under the device, whose size decides it.
 _MAX_PLANS = 512
 _plans = {}
 
@@ -420,7 +420,7 @@ def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: flo
            _sig(parents))
     plan = _plans.get(key) or _remember(key, _plan_attend(q, k_pages, v_pages, page_table, lens,
                                                           parents))
-    lay, N, R, Hq, q_row, q_head, max_pages, ws_bytes, default_scale = plan
+    lay, N, R, Hq, q_row, q_head, max_pages, default_scale = plan
     torch = _torch()
     others = dict(k_pages=k_pages, v_pages=v_pages, page_table=page_table, lens=lens,
                   parents=parents, workspace=workspace)
@@ -437,6 +437,10 @@ def attend_block(q, k_pages, v_pages, page_table, lens, parents=None, scale: flo
         out = AttendResult(torch.empty(q.shape, dtype=q.dtype, device=device),
                            torch.empty(q.shape[:3], dtype=torch.float32, device=device)
                            if want_lse else None, _new_status(dev))
+    ws_key = ("attend workspace", dev, key)
+    ws_bytes = _plans.get(ws_key)
+    if ws_bytes is None:  # (0 for sizes that the call itself refuses)
+        ws_bytes = _remember(ws_key, psi_attend_block_workspace_bytes(lay, N, R, Hq, max_pages))
     if workspace is None or _nbytes(workspace) < ws_bytes:
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=device)
     st = psi_attend_block(lay, k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
@@ -454,9 +458,7 @@ def _plan_attend(q, k_pages, v_pages, page_table, lens, parents):
     Hq, D = q.shape[2], lay.head_dim
     q_row, q_head = _heads("q", q, N, R, Hq, D, k_pages.dtype)
     max_pages = page_table.shape[1]
-    # (0 for sizes that the call itself refuses)
-    return lay, N, R, Hq, q_row, q_head, max_pages, \
-        psi_attend_block_workspace_bytes(lay, N, R, Hq, max_pages), D ** -0.5
+    return lay, N, R, Hq, q_row, q_head, max_pages, D ** -0.5
 
 
 def cache_commit(k_pages, v_pages, page_table, lens, path_nodes, path_len, stream=None,
