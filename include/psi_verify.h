@@ -427,7 +427,8 @@ size_t psi_attend_block_workspace_bytes(const psi_cache_layout *layout, int32_t 
  *   o = sum_t p_t v_t,  p = softmax over the seen t of scale * (q . k_t)
  * with kv head h / (q_heads / kv_heads) for query head h.  What a row does
  * not see has no influence on it, whatever it holds.  A row that sees
- * nothing (invalid parents; no valid page) gives zeros.
+ * nothing (invalid parents; no valid page), or whose scores are all -inf,
+ * gives zeros.
  *
  * q         as in psi_cache_append; the block's keys and values are in the
  *           pages already.
@@ -435,9 +436,12 @@ size_t psi_attend_block_workspace_bytes(const psi_cache_layout *layout, int32_t 
  * out_lse   float [N][R][q_heads] or NULL: log of the sum of
  *           exp(scale * q . k_t) over the seen t, -inf for none.
  * Scores, the softmax and the sums are float; bf16 weights p are rounded to
- * bf16 for the product with v.  The same call gives the same bits, and a
- * sequence's bits do not depend on what the other sequences hold (N, R and
- * the tables' width decide how a length is divided among CTAs).
+ * bf16 for the product with v.  A score's rounding, 2^-24 of its size, is an
+ * error of p's exponent, so scores should stay well below 2^20; sums of
+ * bf16 values are finite for |v| times the length below 2^67.
+ * The same call gives the same bits, and a sequence's bits do not depend on
+ * what the other sequences hold (N, R and the tables' width decide how a
+ * length is divided among CTAs).
  * Limits: as psi_cache_append; q_heads a multiple of kv_heads; scale finite.
  */
 psi_status psi_attend_block(const psi_cache_layout *layout, const void *k_pages,

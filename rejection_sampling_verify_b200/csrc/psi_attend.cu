@@ -7,9 +7,10 @@
 // leaves a partial result that join_kernel adds up.
 //
 // bf16 heads of up to 128 elements run on the tensor cores
-// (psi_attend_tc.cu); float32 and larger heads here, on the FMA pipe: bf16 products of any kind would cost float32 half of its digits.
+// (psi_attend_tc.cu); float32 and larger heads here, on the FMA pipe: bf16
+// products of any kind would cost float32 half of its digits.
 // Latency bounds small float32 batches: 4 sequences of up to 2,500 positions,
-// 5 rows of 16 query and 2 kv heads of 64 (5.3 MB), take 28 us.
+// 5 rows of 16 query and 2 kv heads of 64 (5.3 MB), take 25 us.
 #include <math.h>
 
 #include <algorithm>
@@ -410,11 +411,19 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
   if (p.tc) attend_tc_rows(rows, &p);
   p.row_tiles = (rows + p.rows - 1) / p.rows;
   const int64_t base = (int64_t)N * kv_heads * p.row_tiles;
-  // CTAs that the device holds at once, and a sequence's tiles by the table's
-  // width.  A range is an SM's even share of all that the tables could hold:
-  // a CTA costs about as much as five tiles beyond its own (finer ranges, for
-  // two to six CTAs in turn, took up to 30 % longer).  Where there are few
-  // sequences, those far shorter than their tables get shorter ranges.
+  // CTAs that the device works on at once (8 to an SM on the FMA pipe, which
+  // small heads fit; float32 heads of 128 fit two), and a sequence's tiles by
+  // the table's width.  A range is an SM's even share of all that the tables
+  // could hold: a CTA costs about as much as five tiles beyond its own (finer
+  // ranges, for two to six CTAs in turn, took up to 30 % longer).
+  // Where there are few sequences, those far shorter than their tables get
+  // shorter ranges, down to `least` tiles.  With the tables' even share as the
+  // least, 8 sequences of 250 to 4,100 positions and 9 rows take 62.7 us in
+  // tables of 32,768 positions and 29.9 in tables of their own; with `least`
+  // as it is, 28.7 and 28.8; with one tile, 29.0 and 29.2.  One tile is better
+  // for 8 of 100 to 900 in tables of 8,192 (20.2 us against 23.4) and for 32
+  // of 100 to 4,000 (65 against 75), worse for 16 single tokens (25.0 against
+  // 24.2).
   const int64_t fill = (int64_t)device_sm_count() * (!p.tc ? 8 : p.groups == 1 ? 2 : 1);
   p.tile = p.tc ? kTcTile : 2 * kTokTile;
   const int64_t tiles = (capacity + p.tile - 1) / p.tile;
@@ -422,7 +431,10 @@ AttendPlan plan_attend(int32_t N, int32_t R, int32_t q_heads, int32_t kv_heads, 
   p.least = (int32_t)(2 * base >= fill ? per : std::min<int64_t>(8, ((p.tc ? 32 : 8) * base + fill - 1) / fill));
   p.splits = (int32_t)std::min<int64_t>((tiles + per - 1) / per, kMaxSplits);
   p.ctas = base * p.splits;
-  // few enough CTAs that the order of ragged lengths decides when the last one ends
+  // Few enough CTAs that the order of ragged lengths decides when the last one
+  // ends: without it 16 trees of 65 rows take 174 us against 134, 64 sequences
+  // of 128 to 2,048 positions and 9 rows 72.7 against 66.9, 8 sequences 28.5
+  // against 28.8.  (A warp orders at most two lengths a lane.)
   p.ordered = N > 1 && N <= kOrdered && p.ctas < 8 * fill;
   const size_t parts = (size_t)N * R * q_heads * p.splits;
   p.workspace = p.splits > 1 ? parts * (sizeof(float) * D + sizeof(float2)) : 0;

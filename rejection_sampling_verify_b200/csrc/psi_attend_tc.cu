@@ -1,13 +1,14 @@
-// psi_attend_tc.cu - block attention on the tensor cores: bf16, heads of 64
-// or 128 elements.
+// psi_attend_tc.cu - block attention on the tensor cores: bf16, heads of up
+// to 128 elements.
 //
 // With few query rows and many positions the positions take the tensor
 // core's 128 rows.  For a tile of 128 positions and NT packed rows:
 //   S^T [128 x NT] = K [128 x D] Q^T        (K as it lies in the pages)
 //   P^T            = 2^(S^T - ref)          (one thread per position)
 //   O^T [D x NT]  += V^T [D x 128] P^T
-// so any number of packed rows wastes at most 15 columns, all 128 threads
-// of the softmax work, and V is read as it lies in the pages too.
+// so packed rows are rounded up to 16 only (those of more than one group are
+// dealt evenly and rounded in each: 161 rows take four groups of 48), all 128
+// threads of the softmax work, and V is read as it lies in the pages too.
 //
 // Floats keep their precision wherever they lie, so the reference of the
 // exponents need not be the running maximum: a row's reference is one score
@@ -15,9 +16,10 @@
 // masked), and is raised (and O^T rescaled) only when a score exceeds it by
 // 2^60.  A tile then costs no reduction over its positions, one barrier tells
 // that nothing has to be raised, and the sums stay below 2^60 times the
-// length.  Weights are rounded to bf16 (half a step
-// of 2^-8) for the product, as its operand must be; the sums take them
-// unrounded.
+// length (finite as long as a value times the length stays below 2^67).  A
+// score carries its rounding, 2^-24 of its size, into the exponent.  Weights
+// are rounded to bf16 (half a step of 2^-8) for the product, as its operand
+// must be; the sums take them unrounded.
 //
 // Loads: where pages are multiples of 8 slots, a tile is a few boxes of a
 // tensor map over the pool (TMA writes the swizzled operand directly, one
@@ -38,16 +40,18 @@
 // CTAs to an SM; more make CTAs of two groups, one to an SM, whose products
 // share the tiles of keys and values (twice the work per loaded tile).  The
 // two groups take turns at the exponentials (133 against 144 us for the trees
-// below).
+// below when it was made).
 //
 // What bounds it, measured with 32 query and 8 kv heads of 128:
 //  - few rows, long lengths: memory.  Two sequences of 65,000 and 131,000
-//    positions, one row each: 136 us, 5.9 TB/s.
-//  - 256 sequences of 128 to 2,048 positions, blocks of 9 rows: 235 us, 5.05 TB/s, mostly
-//    the loads' latency.  At 236 us, one step of each tile's products in place
-//    of all left 213, constant weights in the unmasked tiles 229, both 210.
-//  - 16 trees of 65 rows, 1,000 to 8,200 positions: 138 us, 569 TFLOP/s, the exponentials
-//    and the products in turn.
+//    positions, one row each: 134 us, 6.0 TB/s.
+//  - 256 sequences of 128 to 2,048 positions, blocks of 9 rows: 232 us, 5.1
+//    TB/s, mostly the loads' latency.  At 236 us, one step of each tile's
+//    products in place of all left 213, constant weights in the unmasked tiles
+//    229, both 210.
+//  - 16 trees of 65 rows, 1,000 to 8,200 positions: 134 us, 584 TFLOP/s, the
+//    exponentials and the products in turn: the tensor pipe is busy for 37 % of
+//    the cycles.
 #include <cuda.h>
 #include <math.h>
 

@@ -14,7 +14,7 @@ namespace {
 // A node never moves to a later slot and the path ascends, so a store never
 // lands on a column that this thread has yet to load.
 // Measured with the resize that follows: 16 trees in 36 layers, 19 MB, take
-// 14 us, which latency bounds; 64 trees, 151 MB, take 40 us, 3.8 TB/s.
+// 13 us, which latency bounds; 64 trees, 151 MB, take 39 us, 3.8 TB/s.
 constexpr int kCommitThreads = 256;
 constexpr int kCommitBatch = 8;
 static_assert(PSI_MAX_BLOCK_ROWS <= kCommitThreads, "one node per thread");
@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(kPageThreads) fork_kernel(ForkArgs a) {
 }
 
 // The partial pages' filled slots, one CTA per (fork, layer, pool): a plain
-// copy that memory bounds (64 forks in 36 layers, 585 MB: 113 us with the
-// bookkeeping above, 5.2 TB/s).
+// copy that memory bounds (64 forks in 36 layers, 585 MB: 111 us with the
+// bookkeeping above, 5.3 TB/s).
 constexpr int kCopyThreads = 256;
 __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(ForkArgs a) {
   pdl_wait();
