@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a
 // CTA: two when there are rows enough to fill the device, one otherwise (four
 // warps a CTA wait for fewer than eight would: 95 against 99 us when it was
 // made, for 17,408 rows of 32 + 2 x 8 heads of 128; 93 us now, 4.6 TB/s).  The
-// float32 variants spill 110 to 160 bytes a thread.
+// float32 variants spill 112 to 144 bytes a thread.
 template <typename Bits, int kWidth, int kRows, bool kInterleaved>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(AppendArgs a) {
   constexpr int kWarps = kAppendThreads / 32 / kRows;  // per row
