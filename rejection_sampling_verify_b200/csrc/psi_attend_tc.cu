@@ -645,6 +645,13 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
         *reinterpret_cast<uint4 *>(pt + c / 4 * 2048) =
             make_uint4(packed[c], packed[c + 1], packed[c + 2], packed[c + 3]);
       if (kTma && bad_page && t < end && !there) {  // (nor is what lies in place of a bad page)
+        // The stage may still hold an earlier tile, whose loads this wait's
+        // parity could not tell from the next tile's: the product that reads it
+        // comes first.  (Waited for already where it is as old as this buffer's
+        // of P^T.)
+        static_assert(T::kPBufs <= 2, "the previous tile's product is the only one in question");
+        if (T::kVStages < T::kPBufs && i >= 1)
+          wait_or_give_up(&bar.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
         const int slot = i % T::kVStages;
         wait_or_give_up(&bars->v_full[slot], (i / T::kVStages) & 1, gave_up);
         uint8_t *v = vring + slot * T::kTile + st * 128;
