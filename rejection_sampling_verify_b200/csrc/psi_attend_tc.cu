@@ -103,6 +103,14 @@ struct TcShape {
   static constexpr int kSoftRegs = kGroups == 1 ? 168 : 200, kLoadRegs = kGroups == 1 ? 88 : 104;
   static constexpr int kNeed = kGroups * 3 * NT;  // columns of tensor memory
   static constexpr int kCols = kNeed <= 64 ? 64 : kNeed <= 128 ? 128 : kNeed <= 256 ? 256 : 512;
+  // The values' row of a position without a page is zeroed by the warp that
+  // issues their products, or with two groups by the position's own thread of
+  // the softmax, whose wait for the stage is sound where the product that read
+  // it last has been waited for: with no more buffers of P^T than stages.
+  // (Which one is a matter of registers: the batch below takes 230 us, and 237
+  // with it in the softmax; the trees 134, and 142 with it in the issuer.)
+  static constexpr bool kIssuerZeroes = kGroups == 1;
+  static_assert(kIssuerZeroes || kVStages >= kPBufs, "");
   static_assert(kStages >= 2 && kNeed <= (kGroups == 1 ? 256 : 512) && NT % 16 == 0, "");
 };
 
@@ -113,6 +121,7 @@ struct TcBarriers {
   uint64_t k_full[3], v_full[3], k_free[3], v_free[3], q_full, drained[2];
   GroupBarriers group[2];
   uint32_t tmem, gave_up, fix;
+  uint32_t missing;  // some position of the range has no page
   uint32_t fix_tokens[kBlockWords];  // the block's positions whose values are not finite
 };
 
@@ -247,6 +256,21 @@ struct Loader {
   }
 };
 
+// Zeroes the rows of a tile of values whose positions, t0 and on, have no page.
+// (Out of line: it is rare, and the registers are the softmax's.  Numbers only:
+// the address of a kernel argument would put them all into memory.)
+template <int D>
+__device__ __noinline__ void zero_missing(const int32_t *table, int page_size, int num_pages, int t0,
+                                          int rows, uint8_t *v) {
+  for (int x = threadIdx.x % 32; x < rows; x += 32) {
+    const int32_t p = table[(t0 + x) / page_size];
+    if (p >= 0 && p < num_pages) continue;
+    for (int c = 0; c < D / 8; ++c)
+      *reinterpret_cast<uint4 *>(v + c / 8 * (kTok * 128) + x * 128 + c % 8 * 16) =
+          make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <int NT, int D, bool kTma, int kGroups>
 __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 1 ? 2 : 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -326,6 +350,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       mbar_init(&bars->q_full, kGroups * kSoft);
       bars->gave_up = 0;
       bars->fix = 0;
+      bars->missing = 0;
       for (int w = 0; w < kBlockWords; ++w) bars->fix_tokens[w] = 0;
       fence_mbar_init();
     }
@@ -335,7 +360,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
   __syncthreads();
   __syncwarp();
   const uint32_t tmem = bars->tmem;
-  volatile uint32_t *gave_up = &bars->gave_up;
+  volatile uint32_t *gave_up = &bars->gave_up, *missing = &bars->missing;
 
   if (tiles > 0 && warp >= kLoadWarp) {
     shrink_registers<T::kLoadRegs>();
@@ -406,6 +431,13 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
           }
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
+          if (kTma && T::kIssuerZeroes && !keys && *missing) {
+            // nor is what lies in place of a page that is not there
+            zero_missing<D>(table, a.g.page_size, a.g.num_pages, begin + i * kTok,
+                            filled < kTok ? filled : kTok, ring + slot * T::kTile);
+            fence_async_shared();
+            __syncwarp();
+          }
           if (lane != 0) continue;
           fence_async_shared();
           tc_fence_after();
@@ -489,6 +521,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
     if (a.dev_status && (bad_page || (want > cap && st == 0)))
       atomicOr(a.dev_status, PSI_DEV_BAD_PAGE);
     bad_page = named_or(sync, kSoft, bad_page);
+    if (T::kIssuerZeroes && bad_page && st == 0) *missing = 1;
     if (!parents) {  // a chain: position x is seen by the rows from x * G on
       for (int i = st; i < a.R * T::kMaskWords; i += kSoft) {
         const int w = i % T::kMaskWords, first = i / T::kMaskWords * G - row0 - w * 32;
@@ -644,14 +677,7 @@ __global__ void __launch_bounds__(TcShape<NT, D, kGroups>::kThreads, kGroups == 
       for (int c = 0; c < NT / 2; c += 4)
         *reinterpret_cast<uint4 *>(pt + c / 4 * 2048) =
             make_uint4(packed[c], packed[c + 1], packed[c + 2], packed[c + 3]);
-      if (kTma && bad_page && t < end && !there) {  // (nor is what lies in place of a bad page)
-        // The stage may still hold an earlier tile, whose loads this wait's
-        // parity could not tell from the next tile's: the product that reads it
-        // comes first.  (Waited for already where it is as old as this buffer's
-        // of P^T.)
-        static_assert(T::kPBufs <= 2, "the previous tile's product is the only one in question");
-        if (T::kVStages < T::kPBufs && i >= 1)
-          wait_or_give_up(&bar.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, gave_up);
+      if (kTma && !T::kIssuerZeroes && bad_page && t < end && !there) {
         const int slot = i % T::kVStages;
         wait_or_give_up(&bars->v_full[slot], (i / T::kVStages) & 1, gave_up);
         uint8_t *v = vring + slot * T::kTile + st * 128;
