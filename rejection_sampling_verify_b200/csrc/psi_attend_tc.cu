@@ -44,13 +44,13 @@
 //
 // What bounds it, measured with 32 query and 8 kv heads of 128:
 //  - few rows, long lengths: memory.  Two sequences of 65,000 and 131,000
-//    positions, one row each: 134 us, 6.0 TB/s.
-//  - 256 sequences of 128 to 2,048 positions, blocks of 9 rows: 232 us, 5.1
+//    positions, one row each: 135 us, 5.9 TB/s.
+//  - 256 sequences of 128 to 2,048 positions, blocks of 9 rows: 230 us, 5.2
 //    TB/s, mostly the loads' latency.  At 236 us, one step of each tile's
 //    products in place of all left 213, constant weights in the unmasked tiles
 //    229, both 210.
-//  - 16 trees of 65 rows, 1,000 to 8,200 positions: 134 us, 584 TFLOP/s, the
-//    exponentials and the products in turn: the tensor pipe is busy for 37 % of
+//  - 16 trees of 65 rows, 1,000 to 8,200 positions: 133 us, 590 TFLOP/s, the
+//    exponentials and the products in turn: the tensor pipe is busy for 36 % of
 //    the cycles.
 #include <cuda.h>
 #include <math.h>
@@ -108,7 +108,7 @@ struct TcShape {
   // the softmax, whose wait for the stage is sound where the product that read
   // it last has been waited for: with no more buffers of P^T than stages.
   // (Which one is a matter of registers: the batch below takes 230 us, and 237
-  // with it in the softmax; the trees 134, and 142 with it in the issuer.)
+  // with it in the softmax; the trees 133, and 142 with it in the issuer.)
   static constexpr bool kIssuerZeroes = kGroups == 1;
   static_assert(kIssuerZeroes || kVStages >= kPBufs, "");
   static_assert(kStages >= 2 && kNeed <= (kGroups == 1 ? 256 : 512) && NT % 16 == 0, "");
